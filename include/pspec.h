@@ -8,6 +8,13 @@
  *   pspec_verify_rejection    target verification, rejection rule
  *   pspec_build_draft_batch   parallel-draft batch construction
  *
+ * and what a decode step needs next to them (pspec_sample_drafts and the three below):
+ *
+ *   pspec_append_kv           keys and values into the paged cache at the draft batch's
+ *                             slots, rotated to its positions, 4-bit or as they are
+ *   pspec_attend              attention of a ragged batch over the 4-bit paged cache
+ *   pspec_sample_filtered     token draw under temperature, top-k, top-p and min-p
+ *
  * Sources (page title, section):
  *   "Capstone 14: speculative decoding inference server", section "Concept": the target
  *     checks the k drafts in one forward pass and an accepted prefix replaces the greedy
@@ -72,6 +79,9 @@ typedef enum { PSPEC_F32 = 0, PSPEC_BF16 = 1 } pspec_dtype;
 #define PSPEC_DEVERR_LAYOUT 0x8        /* qsl_in not an offset array, or a sequence with
                                           fewer than K+1 verify rows */
 #define PSPEC_DEVERR_KLEN_RANGE 0x20   /* k_len[i] outside [0, K]: clamped into it */
+#define PSPEC_DEVERR_PARAM_RANGE 0x40  /* a sampling parameter that is NaN, or a negative or
+                                          infinite temperature: that filter is off (for
+                                          the temperature: 1) */
 
 /* Row kinds written to pspec_build_args.row_kind. */
 #define PSPEC_ROW_CTX 0   /* context row: accepted token paired with its target hidden */
@@ -441,6 +451,177 @@ PSPEC_API void pspec_set_segment_elems(long long elems);
    draw; after the single launch of the early-exit path), so that a caller can time each
    launch with CUDA events.  NULL turns it off.  Process-wide; the caller owns the event. */
 PSPEC_API void pspec_set_split_event(cudaEvent_t event);
+
+/*
+ * The paged KV cache in 4 bits ("e2m1"): per page, kv head and token, D values as blocks of
+ * 16 along the head dimension, each block with one scale.
+ *   pages         [num_blocks, Hkv, block_size, D/2] bytes; byte b of a row holds element 2b
+ *                 in its low and 2b+1 in its high nibble; a nibble is sign, two exponent bits
+ *                 and one mantissa bit (magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6)
+ *   block scales  [num_blocks, Hkv, block_size, D/16] bytes, e4m3 (finite, not negative)
+ *   head scales   [Hkv] fp32, positive and finite, or NULL for 1
+ *   value         code * block scale * head scale
+ * Quantisation of x: s = e4m3(max|x / g| / 6), rounded to nearest (ties to even), at most
+ * 448; code = e2m1(x / (g s)), ties to the even code, at most 6; decided as if computed
+ * exactly.  A block whose scale rounds to 0 stores zeros; NaN elements store 0 and count as 0
+ * in the maximum.
+ * A token's slot is block * block_size + offset, as pspec_build_draft_batch writes them.
+ */
+typedef enum { PSPEC_CACHE_ROWS = 0, PSPEC_CACHE_E2M1 = 1 } pspec_cache_kind;
+
+/*
+ * Keys and values appended to the paged cache, with the position rotation on the way.
+ *
+ * Row t < T of k and v (Hkv heads of D elements) goes to slot slot_mapping[t]; the first
+ * `rot` elements of each key head (and of each head of the optional q, which goes to q_out)
+ * are rotated by the angles positions[t] * inv_freq[j], j < rot/2: elements (j, j + rot/2),
+ * or (2j, 2j+1) when `interleaved`, as (a cos - b sin, b cos + a sin).  Angles are formed and
+ * reduced in fp64.  A row whose slot is PSPEC_PADDING_SLOT_ID is skipped whole: no cache
+ * write, its rows of q_out, k_out and v_out left as they were.  A slot below -1 or past the
+ * cache skips the row the same way and sets PSPEC_DEVERR_BLOCK_RANGE.  A slot given to two
+ * rows of one call ends with bytes of either (the batch builder never does so); every other
+ * slot of the cache keeps its content.
+ * PSPEC_CACHE_ROWS stores the rows in their own dtype (pages [num_blocks, Hkv, block_size,
+ * D], the scale arrays unused); PSPEC_CACHE_E2M1 stores the 4-bit form above.  k_out and
+ * v_out (optional, contiguous [T, Hkv, D], rows' dtype) receive the values the cache now
+ * stands for, for callers that attend to the same chunk in 16 bits.
+ * One launch.  Outputs must not overlap inputs (PSPEC_ERR_INVALID_ARG).  Limits: D a multiple
+ * of 16, D <= 512, rot even, 0 <= rot <= D (PSPEC_ERR_INVALID_ARG otherwise).  Row strides
+ * are in elements and at least H*D; rows, pages and outputs of any element alignment are
+ * taken, 16-byte aligned ones (bases, and strides times element size) are read and written
+ * fastest.  E2M1 pages, and PSPEC_CACHE_ROWS pages, must be 16-byte aligned.
+ */
+typedef struct {
+  int T;                       /* rows; T = 0 is a no-op */
+  int Hq;                      /* query heads (ignored when q is NULL) */
+  int Hkv;                     /* key / value heads, >= 1 */
+  int D;                       /* head dimension */
+  int rot;                     /* rotated elements per head, 0 for none */
+  int interleaved;             /* 0: pairs (j, j + rot/2); 1: pairs (2j, 2j+1) */
+  pspec_dtype dtype;           /* dtype of q, k, v and their outputs */
+  pspec_cache_kind cache;
+  int block_size;              /* tokens per page, >= 1 */
+  int num_blocks;              /* pages, >= 1 */
+  long long q_stride;          /* elements between rows of q / k / v */
+  long long k_stride;
+  long long v_stride;
+  const void *q;               /* [T, Hq, D], optional (NULL) */
+  const void *k;               /* [T, Hkv, D] */
+  const void *v;               /* [T, Hkv, D] */
+  const int32_t *positions;    /* [T] */
+  const int64_t *slot_mapping; /* [T] */
+  const float *inv_freq;       /* [rot/2] (may be NULL when rot is 0) */
+  void *k_pages;
+  void *v_pages;
+  void *k_block_scales;        /* PSPEC_CACHE_E2M1 only */
+  void *v_block_scales;
+  const float *k_scale;        /* [Hkv] head scales or NULL (PSPEC_CACHE_E2M1 only) */
+  const float *v_scale;
+  void *q_out;                 /* [T, Hq, D] contiguous out (required with q) */
+  void *k_out;                 /* [T, Hkv, D] contiguous out, optional */
+  void *v_out;                 /* [T, Hkv, D] contiguous out, optional */
+  int32_t *err;                /* device error word (required) */
+} pspec_append_args;
+
+PSPEC_API pspec_status pspec_append_kv(const pspec_append_args *args, cudaStream_t stream);
+
+/*
+ * Attention of a ragged batch over the 4-bit paged cache.
+ *
+ * Sequence i owns query rows [qsl[i], qsl[i+1]) and keys 0 .. seq_lens[i]-1, key j at
+ * block_table[i][j / block_size], offset j % block_size.  Row t sees the keys j <=
+ * positions[t], j < seq_lens[i] (the draft batch's positions and lengths as they are).
+ * Query head h reads kv head h / (Hq / Hkv).
+ *   out[t][h] = sum_j softmax_j(scale * q[t][h] . k_j) v_j,  lse[t][h] = ln sum_j exp(...)
+ * A row that sees no key gets zeros and lse = -inf.  Rows of kind PSPEC_ROW_REJ and
+ * PSPEC_ROW_PAD (when row_kind is given), and rows of no sequence, are left as they were.
+ * Statistics and sums are fp32; products of the cache's values (exact in fp16) with the
+ * queries and the probabilities run on fp16 tensor cores with fp32 sums: bf16 queries are
+ * exact there after a power-of-two scaling per row and probabilities are rounded to 11 bits;
+ * fp32 queries and their probabilities are split into two fp16 terms.
+ * D is 64 or 128 (PSPEC_ERR_UNSUPPORTED otherwise).  Invalid values on the device: a qsl that
+ * is not an offset array into [0, T] skips the offending sequence (PSPEC_DEVERR_LAYOUT; a row
+ * that two others then claim holds either's result); a
+ * length past the block table is cut to it and a block id outside [0, num_blocks) hides that
+ * page's keys (PSPEC_DEVERR_BLOCK_RANGE).  Keys past a row's position may hold anything (a NaN
+ * or negative block scale counts as 0); keys past seq_lens are not read.
+ * One launch: the keys of all sequences and heads are dealt out evenly over the GPU in runs
+ * of 64; the CTA that finishes a row tile's last run joins the tile's partial results, in key
+ * order.  Workspace: pspec_attend_workspace_bytes() bytes for any batch, 256-byte aligned,
+ * zero-filled once before first use (each call leaves its counters at zero).  Calls that
+ * share one workspace must not overlap on the GPU.
+ */
+typedef struct {
+  int T;                       /* rows of q */
+  int B;                       /* sequences; B = 0 or T = 0 is a no-op */
+  int Hq;                      /* query heads, a multiple of Hkv */
+  int Hkv;
+  int D;                       /* head dimension, 64 or 128 */
+  pspec_dtype dtype;           /* dtype of q and out */
+  int block_size;
+  int num_blocks;
+  int max_blocks;              /* columns of block_table */
+  float scale;                 /* factor of the dot products, finite */
+  long long q_stride;          /* elements between rows of q, >= Hq*D */
+  const void *q;               /* [T, Hq, D] */
+  const void *k_pages;         /* the cache, PSPEC_CACHE_E2M1; 16-byte aligned */
+  const void *v_pages;
+  const void *k_block_scales;  /* 16-byte aligned */
+  const void *v_block_scales;
+  const float *k_scale;        /* [Hkv] or NULL */
+  const float *v_scale;
+  const int32_t *block_table;  /* [B, max_blocks] */
+  const int32_t *qsl;          /* [B+1] */
+  const int32_t *positions;    /* [T] */
+  const int32_t *seq_lens;     /* [B] */
+  const uint8_t *row_kind;     /* [T] or NULL */
+  void *out;                   /* [T, Hq, D] contiguous out */
+  float *lse;                  /* [T, Hq] out, optional */
+  int32_t *err;                /* device error word (required) */
+} pspec_attend_args;
+
+PSPEC_API size_t pspec_attend_workspace_bytes(void);
+PSPEC_API pspec_status pspec_attend(const pspec_attend_args *args, void *workspace,
+                                    size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Token draw under a request's sampling parameters, from given uniforms.
+ *
+ * For row (i, k) of logits [B, K, ld]: w_t = exp((x_t - max x) / temperature[i]); order the
+ * tokens by (x descending, id ascending) and keep the longest prefix of that order whose
+ * every member has
+ *   rank < top_k[i]                                    (top_k <= 0: off)
+ *   mass before it < top_p[i] * mass of the top_k set  (top_p >= 1: off)
+ *   w_t >= min_p[i]                                    (min_p <= 0: off)
+ * the first token always; token = the smallest kept id whose cumulative mass in id order
+ * exceeds uniforms[i][k] times the kept mass (if rounding leaves none, the last kept id with
+ * mass), the convention of pspec_sample_drafts.  temperature 0 takes the argmax, lowest id on
+ * ties.  Masses are fp64 sums of fp64 exponentials: a token is the exactly computed draw
+ * unless its border is within about 1e-11 of the uniform.  NaN logits count as -inf; a row of
+ * -inf alone gives token 0 with probability 0; if logits are +inf, those tokens share the
+ * mass equally.  probs (optional) is the drawn token's share of the kept mass.  Any parameter
+ * array may be NULL (temperature 1, filters off).  One launch, a cluster of CTAs per row; no
+ * workspace.  V is at most PSPEC_FILTER_MAX_V (PSPEC_ERR_UNSUPPORTED above).
+ */
+#define PSPEC_FILTER_MAX_V (1 << 24)
+typedef struct {
+  int B;                       /* sequences; B = 0 is a no-op */
+  int K;                       /* rows per sequence, >= 1 */
+  int V;                       /* vocabulary size, >= 1 */
+  long long ld;                /* row stride in elements, >= V */
+  pspec_dtype dtype;
+  const void *logits;          /* [B, K, ld] */
+  const float *uniforms;       /* [B, K] in [0,1) */
+  const float *temperature;    /* [B] or NULL */
+  const int32_t *top_k;        /* [B] or NULL */
+  const float *top_p;          /* [B] or NULL */
+  const float *min_p;          /* [B] or NULL */
+  int32_t *tokens;             /* [B, K] out */
+  float *probs;                /* [B, K] out, optional */
+  int32_t *err;                /* device error word (required) */
+} pspec_filter_args;
+
+PSPEC_API pspec_status pspec_sample_filtered(const pspec_filter_args *args, cudaStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -15,8 +15,10 @@ from __future__ import annotations
 
 import importlib
 
-_API_NAMES = ("Workspace", "build_draft_batch", "sample_drafts", "step", "verify_greedy",
-              "verify_rejection")
+_API_NAMES = ("KVCache", "Workspace", "append_kv", "attend", "attend_workspace",
+              "build_draft_batch", "prepare_append_kv", "prepare_attend",
+              "prepare_sample_filtered", "sample_drafts", "sample_filtered", "step",
+              "verify_greedy", "verify_rejection")
 
 
 def __getattr__(name):

@@ -20,9 +20,12 @@ PSPEC_F32, PSPEC_BF16 = 0, 1
 PSPEC_DEVERR_TOKEN_RANGE, PSPEC_DEVERR_ACCEPT_RANGE = 0x1, 0x2
 PSPEC_DEVERR_BLOCK_RANGE, PSPEC_DEVERR_LAYOUT = 0x4, 0x8
 PSPEC_DEVERR_KLEN_RANGE = 0x20
+PSPEC_DEVERR_PARAM_RANGE = 0x40
+PSPEC_CACHE_ROWS, PSPEC_CACHE_E2M1 = 0, 1
 PSPEC_ROW_CTX, PSPEC_ROW_NTP, PSPEC_ROW_MASK, PSPEC_ROW_REJ, PSPEC_ROW_PAD = range(5)
 PSPEC_PADDING_SLOT_ID = -1
 PSPEC_MAX_K = 31
+PSPEC_FILTER_MAX_V = 1 << 24
 
 EXPORTED = (
     "pspec_verify_workspace_bytes", "pspec_verify_greedy", "pspec_verify_rejection",
@@ -32,7 +35,8 @@ EXPORTED = (
     "pspec_set_segment_elems", "pspec_set_split_event", "pspec_verify_greedy_noalloc",
     "pspec_step_greedy", "pspec_step_rejection", "pspec_set_step_fusion",
     "pspec_set_tail_split", "pspec_last_cluster_size", "pspec_get_options",
-    "pspec_verify_workspace_bytes_opt",
+    "pspec_verify_workspace_bytes_opt", "pspec_append_kv", "pspec_attend_workspace_bytes",
+    "pspec_attend", "pspec_sample_filtered",
 )
 
 
@@ -84,6 +88,39 @@ class pspec_build_args(ctypes.Structure):
     ]
 
 
+class pspec_append_args(ctypes.Structure):
+    _fields_ = [
+        ("T", _I), ("Hq", _I), ("Hkv", _I), ("D", _I), ("rot", _I), ("interleaved", _I),
+        ("dtype", _I), ("cache", _I), ("block_size", _I), ("num_blocks", _I),
+        ("q_stride", ctypes.c_longlong), ("k_stride", ctypes.c_longlong),
+        ("v_stride", ctypes.c_longlong),
+        ("q", _P), ("k", _P), ("v", _P), ("positions", _P), ("slot_mapping", _P),
+        ("inv_freq", _P), ("k_pages", _P), ("v_pages", _P), ("k_block_scales", _P),
+        ("v_block_scales", _P), ("k_scale", _P), ("v_scale", _P), ("q_out", _P),
+        ("k_out", _P), ("v_out", _P), ("err", _P),
+    ]
+
+
+class pspec_attend_args(ctypes.Structure):
+    _fields_ = [
+        ("T", _I), ("B", _I), ("Hq", _I), ("Hkv", _I), ("D", _I), ("dtype", _I),
+        ("block_size", _I), ("num_blocks", _I), ("max_blocks", _I), ("scale", ctypes.c_float),
+        ("q_stride", ctypes.c_longlong),
+        ("q", _P), ("k_pages", _P), ("v_pages", _P), ("k_block_scales", _P),
+        ("v_block_scales", _P), ("k_scale", _P), ("v_scale", _P), ("block_table", _P),
+        ("qsl", _P), ("positions", _P), ("seq_lens", _P), ("row_kind", _P), ("out", _P),
+        ("lse", _P), ("err", _P),
+    ]
+
+
+class pspec_filter_args(ctypes.Structure):
+    _fields_ = [
+        ("B", _I), ("K", _I), ("V", _I), ("ld", ctypes.c_longlong), ("dtype", _I),
+        ("logits", _P), ("uniforms", _P), ("temperature", _P), ("top_k", _P), ("top_p", _P),
+        ("min_p", _P), ("tokens", _P), ("probs", _P), ("err", _P),
+    ]
+
+
 def _load():
     if not os.path.exists(_LIB_PATH):
         raise ImportError(
@@ -129,6 +166,14 @@ def _load():
     lib.pspec_set_segment_elems.restype = None
     lib.pspec_set_split_event.argtypes = [_P]
     lib.pspec_set_split_event.restype = None
+    lib.pspec_append_kv.argtypes = [ctypes.POINTER(pspec_append_args), _P]
+    lib.pspec_append_kv.restype = _I
+    lib.pspec_attend_workspace_bytes.argtypes = []
+    lib.pspec_attend_workspace_bytes.restype = ctypes.c_size_t
+    lib.pspec_attend.argtypes = [ctypes.POINTER(pspec_attend_args), _P, ctypes.c_size_t, _P]
+    lib.pspec_attend.restype = _I
+    lib.pspec_sample_filtered.argtypes = [ctypes.POINTER(pspec_filter_args), _P]
+    lib.pspec_sample_filtered.restype = _I
     return lib
 
 
@@ -471,3 +516,203 @@ def prepare_step(*, target_logits, draft_tokens, out_tokens, accepted_len, bonus
     keep = [target_logits, draft_logits, draft_tokens, uniforms, out_tokens, accepted_len, bonus,
             err, workspace, residual_mass, k_len, dict(build)]
     return PreparedStep(rej, v, b, workspace, keep)
+
+
+# --------------------------------------------------- the cache and sampling operators
+class PreparedCall:
+    """A C entry point with its argument struct filled once: calling it issues the launch on
+    the given stream (a torch.cuda.Stream of the tensors' device, a raw cudaStream_t handle, or
+    None for torch's current stream of that device).  The tensors stay alive with this object
+    and must keep their storage; their contents may change between calls."""
+
+    def __init__(self, name: str, args, tensors, workspace=None):
+        self._name, self._fn, self._args, self._ptr = name, getattr(LIB, name), args, ctypes.byref(args)
+        self._keep = (tensors, workspace)
+        self._tail = () if workspace is None else (_ptr(workspace, torch.uint8, "workspace"),
+                                                   workspace.numel())
+        devices = {t.device for t in tensors if t is not None}
+        if workspace is not None:
+            devices.add(workspace.device)
+        if len(devices) != 1 or next(iter(devices)).type != "cuda":
+            raise ValueError(f"{name}: all tensors must be on one CUDA device, got {sorted(map(str, devices))}")
+        self._device = next(iter(devices))
+
+    def __call__(self, stream=None) -> None:
+        if isinstance(stream, torch.cuda.Stream) and stream.device != self._device:
+            raise ValueError(f"{self._name}: the stream is on {stream.device}, the tensors on {self._device}")
+        if torch.cuda.current_device() != self._device.index:
+            with torch.cuda.device(self._device):        # launches go to the current device
+                st = self._fn(self._ptr, *self._tail, _stream(stream))
+        else:
+            st = self._fn(self._ptr, *self._tail, _stream(stream))
+        if st != PSPEC_OK:
+            raise PspecError(self._name, st)
+
+
+def _shape(t, shape, name):
+    if t is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _rows_layout(t, name, dtype=None):
+    """(T, H, D, row stride) of a [T, H, D] tensor whose rows may be apart (a view of a fused
+    projection), heads and elements dense."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 3:
+        raise ValueError(f"{name} must be a [rows, heads, head_dim] tensor")
+    if t.dtype not in _DT or (dtype is not None and t.dtype != dtype):
+        raise TypeError(f"{name} must be {dtype or 'float32 or bfloat16'}, got {t.dtype}")
+    T, H, D = t.shape
+    if (D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D) or (T > 1 and t.stride(0) < H * D):
+        raise ValueError(f"{name} must have dense heads and rows that do not overlap")
+    return T, H, D, t.stride(0) if T > 1 else H * D
+
+
+def _cache_layout(k_pages, v_pages, k_block_scales, v_block_scales, D):
+    """(cache kind, num_blocks, Hkv, block_size) of the cache tensors, for a head dimension."""
+    if k_pages.dim() != 4 or k_pages.shape != v_pages.shape or k_pages.dtype != v_pages.dtype:
+        raise ValueError("k and v pages must be alike, [num_blocks, heads, block_size, ...]")
+    n, H, bs, w = k_pages.shape
+    if k_pages.dtype == torch.uint8:
+        if w * 2 != D:
+            raise ValueError(f"4-bit pages of head dimension {D} have {D // 2} bytes a row, got {w}")
+        for t, nm in ((k_block_scales, "k_block_scales"), (v_block_scales, "v_block_scales")):
+            if t is None or t.dtype not in (torch.float8_e4m3fn, torch.uint8):
+                raise TypeError(f"{nm} must be float8_e4m3fn (or its bytes) for 4-bit pages")
+            _shape(t, (n, H, bs, D // 16), nm)
+        return PSPEC_CACHE_E2M1, n, H, bs
+    if k_block_scales is not None or v_block_scales is not None:
+        raise ValueError("block scales belong to 4-bit pages (uint8)")
+    if w != D:
+        raise ValueError(f"pages of head dimension {D} have {D} elements a row, got {w}")
+    return PSPEC_CACHE_ROWS, n, H, bs
+
+
+def _call(name, a, tensors, workspace, prepare, stream):
+    c = PreparedCall(name, a, tensors, workspace)
+    if prepare:
+        return c
+    c(stream)
+
+
+def pspec_append_kv(*, k, v, positions, slot_mapping, k_pages, v_pages, err, k_block_scales=None,
+                    v_block_scales=None, k_scale=None, v_scale=None, q=None, inv_freq=None,
+                    interleaved=False, q_out=None, k_out=None, v_out=None, stream=None,
+                    prepare=False):
+    """See include/pspec.h.  k, v (and q): [T, heads, D], rows may be strided.  prepare: return
+    the PreparedCall instead of running it."""
+    T, Hkv, D, ks = _rows_layout(k, "k")
+    _rows_layout(v, "v", k.dtype)
+    _shape(v, k.shape, "v")
+    kind, n, Hc, bs = _cache_layout(k_pages, v_pages, k_block_scales, v_block_scales, D)
+    if Hc != Hkv:
+        raise ValueError(f"the cache has {Hc} heads, k {Hkv}")
+    if kind == PSPEC_CACHE_ROWS and k_pages.dtype != k.dtype:
+        raise TypeError(f"16- or 32-bit pages must have the rows' dtype {k.dtype}, got {k_pages.dtype}")
+    a = pspec_append_args()
+    a.T, a.Hkv, a.D, a.dtype, a.cache = T, Hkv, D, _DT[k.dtype], kind
+    a.block_size, a.num_blocks, a.interleaved = bs, n, int(bool(interleaved))
+    a.k_stride, a.v_stride = ks, _rows_layout(v, "v")[3]
+    a.k, a.v = k.data_ptr(), v.data_ptr()
+    if q is not None:
+        Tq, a.Hq, Dq, a.q_stride = _rows_layout(q, "q", k.dtype)
+        if Tq != T or Dq != D:
+            raise ValueError(f"q must be [{T}, heads, {D}], got {tuple(q.shape)}")
+        if q_out is None:
+            raise ValueError("q needs q_out")
+        _shape(q_out, q.shape, "q_out")
+        a.q, a.q_out = q.data_ptr(), _ptr(q_out, k.dtype, "q_out")
+    elif q_out is not None:
+        raise ValueError("q_out needs q")
+    if inv_freq is not None:
+        if inv_freq.dim() != 1:
+            raise ValueError("inv_freq must be [rot / 2]")
+        a.rot, a.inv_freq = 2 * inv_freq.numel(), _ptr(inv_freq, torch.float32, "inv_freq")
+    _shape(positions, (T,), "positions")
+    _shape(slot_mapping, (T,), "slot_mapping")
+    for t, nm in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        _shape(t, (Hkv,), nm)
+    for t, nm in ((k_out, "k_out"), (v_out, "v_out")):
+        _shape(t, k.shape, nm)
+    a.positions = _ptr(positions, torch.int32, "positions")
+    a.slot_mapping = _ptr(slot_mapping, torch.int64, "slot_mapping")
+    a.k_pages, a.v_pages = _ptr(k_pages, None, "k_pages"), _ptr(v_pages, None, "v_pages")
+    a.k_block_scales = _ptr(k_block_scales, None, "k_block_scales")
+    a.v_block_scales = _ptr(v_block_scales, None, "v_block_scales")
+    a.k_scale, a.v_scale = _ptr(k_scale, torch.float32, "k_scale"), _ptr(v_scale, torch.float32, "v_scale")
+    a.k_out, a.v_out = _ptr(k_out, k.dtype, "k_out"), _ptr(v_out, k.dtype, "v_out")
+    a.err = _ptr(err, torch.int32, "err")
+    return _call("pspec_append_kv", a,
+                 (k, v, positions, slot_mapping, k_pages, v_pages, err, k_block_scales, v_block_scales,
+                  k_scale, v_scale, q, inv_freq, q_out, k_out, v_out), None, prepare, stream)
+
+
+def pspec_attend_workspace_bytes() -> int:
+    return int(LIB.pspec_attend_workspace_bytes())
+
+
+def pspec_attend(*, q, k_pages, v_pages, k_block_scales, v_block_scales, block_table, qsl,
+                 positions, seq_lens, out, err, workspace, scale, k_scale=None, v_scale=None,
+                 row_kind=None, lse=None, stream=None, prepare=False):
+    """See include/pspec.h.  q: [T, Hq, D], rows may be strided.  prepare: return the
+    PreparedCall instead of running it."""
+    T, Hq, D, qs = _rows_layout(q, "q")
+    kind, n, Hkv, bs = _cache_layout(k_pages, v_pages, k_block_scales, v_block_scales, D)
+    if kind != PSPEC_CACHE_E2M1:
+        raise TypeError("attention reads a 4-bit cache (uint8 pages)")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [sequences, blocks]")
+    B, mb = block_table.shape
+    _shape(qsl, (B + 1,), "qsl")
+    _shape(seq_lens, (B,), "seq_lens")
+    _shape(positions, (T,), "positions")
+    _shape(row_kind, (T,), "row_kind")
+    _shape(out, (T, Hq, D), "out")
+    _shape(lse, (T, Hq), "lse")
+    for t, nm in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        _shape(t, (Hkv,), nm)
+    a = pspec_attend_args()
+    a.T, a.B, a.Hq, a.Hkv, a.D, a.dtype = T, B, Hq, Hkv, D, _DT[q.dtype]
+    a.block_size, a.num_blocks, a.max_blocks = bs, n, mb
+    a.scale, a.q_stride, a.q = float(scale), qs, q.data_ptr()
+    a.k_pages, a.v_pages = _ptr(k_pages, None, "k_pages"), _ptr(v_pages, None, "v_pages")
+    a.k_block_scales = _ptr(k_block_scales, None, "k_block_scales")
+    a.v_block_scales = _ptr(v_block_scales, None, "v_block_scales")
+    a.k_scale, a.v_scale = _ptr(k_scale, torch.float32, "k_scale"), _ptr(v_scale, torch.float32, "v_scale")
+    a.block_table = _ptr(block_table, torch.int32, "block_table")
+    a.qsl = _ptr(qsl, torch.int32, "qsl")
+    a.positions = _ptr(positions, torch.int32, "positions")
+    a.seq_lens = _ptr(seq_lens, torch.int32, "seq_lens")
+    a.row_kind = _ptr(row_kind, torch.uint8, "row_kind")
+    a.out, a.lse = _ptr(out, q.dtype, "out"), _ptr(lse, torch.float32, "lse")
+    a.err = _ptr(err, torch.int32, "err")
+    return _call("pspec_attend", a,
+                 (q, k_pages, v_pages, k_block_scales, v_block_scales, block_table, qsl, positions,
+                  seq_lens, out, err, k_scale, v_scale, row_kind, lse), workspace, prepare, stream)
+
+
+def pspec_sample_filtered(*, logits, uniforms, tokens, err, temperature=None, top_k=None,
+                          top_p=None, min_p=None, probs=None, stream=None, prepare=False):
+    """See include/pspec.h.  logits: [B, K, V], rows may be padded.  prepare: return the
+    PreparedCall instead of running it."""
+    if logits.dim() != 3:
+        raise ValueError(f"logits must be [B, K, V], got {tuple(logits.shape)}")
+    K = int(logits.shape[1])
+    Bn, V, ld, dt = _logits_layout(logits, K, "logits")
+    _shape(uniforms, (Bn, K), "uniforms")
+    _shape(tokens, (Bn, K), "tokens")
+    _shape(probs, (Bn, K), "probs")
+    for t, nm in ((temperature, "temperature"), (top_k, "top_k"), (top_p, "top_p"), (min_p, "min_p")):
+        _shape(t, (Bn,), nm)
+    a = pspec_filter_args()
+    a.B, a.K, a.V, a.ld, a.dtype, a.logits = Bn, K, V, ld, dt, logits.data_ptr()
+    a.uniforms = _ptr(uniforms, torch.float32, "uniforms")
+    a.temperature = _ptr(temperature, torch.float32, "temperature")
+    a.top_k = _ptr(top_k, torch.int32, "top_k")
+    a.top_p = _ptr(top_p, torch.float32, "top_p")
+    a.min_p = _ptr(min_p, torch.float32, "min_p")
+    a.tokens = _ptr(tokens, torch.int32, "tokens")
+    a.probs = _ptr(probs, torch.float32, "probs")
+    a.err = _ptr(err, torch.int32, "err")
+    return _call("pspec_sample_filtered", a,
+                 (logits, uniforms, tokens, err, temperature, top_k, top_p, min_p, probs), None,
+                 prepare, stream)

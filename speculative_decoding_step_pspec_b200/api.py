@@ -5,6 +5,8 @@ binding; every step of the method runs in libpspec's kernels.
 """
 from __future__ import annotations
 
+from dataclasses import dataclass
+
 import torch
 
 from . import _binding as _b
@@ -220,3 +222,142 @@ def prepare_step(target_logits: torch.Tensor, draft_tokens: torch.Tensor, build:
                            draft_logits=draft_logits, uniforms=uniforms,
                            residual_mass=o.get("residual_mass"), k_len=k_len, options=options)
     return call, o, bo
+
+
+# --------------------------------------------------- the cache and sampling operators
+@dataclass
+class KVCache:
+    """A paged KV cache: ``k`` and ``v`` are [num_blocks, heads, block_size, head_dim] in the
+    rows' dtype, or [num_blocks, heads, block_size, head_dim / 2] uint8 with two e2m1 codes a
+    byte; then ``*_block_scales`` [num_blocks, heads, block_size, head_dim / 16] are
+    float8_e4m3fn and ``*_scale`` [heads] (or None) fp32."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_block_scales: torch.Tensor | None = None
+    v_block_scales: torch.Tensor | None = None
+    k_scale: torch.Tensor | None = None
+    v_scale: torch.Tensor | None = None
+
+    @classmethod
+    def zeros(cls, num_blocks: int, heads: int, block_size: int, head_dim: int, *, dtype=None,
+              device="cuda", k_scale=None, v_scale=None) -> "KVCache":
+        """A cache of zeros: 4-bit for dtype None, else pages of that dtype."""
+        shape = (num_blocks, heads, block_size)
+        if dtype is not None:
+            return cls(*(torch.zeros((*shape, head_dim), dtype=dtype, device=device) for _ in range(2)))
+        pages = [torch.zeros((*shape, head_dim // 2), dtype=torch.uint8, device=device) for _ in range(2)]
+        scales = [torch.zeros((*shape, head_dim // 16), dtype=torch.float8_e4m3fn, device=device)
+                  for _ in range(2)]
+        return cls(*pages, *scales, k_scale, v_scale)
+
+
+def _err(device) -> torch.Tensor:
+    return torch.zeros((1,), dtype=torch.int32, device=device)
+
+
+def _append(k, v, positions, slot_mapping, cache, q, inv_freq, interleaved, want_values, out,
+            stream, prepare):
+    o = dict(out) if out is not None else {}
+    if out is None:
+        if q is not None:
+            o["q"] = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if want_values:
+            o["k"], o["v"] = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (k, v))
+    if "err" not in o:
+        o["err"] = _err(k.device)
+    c = _b.pspec_append_kv(k=k, v=v, positions=positions, slot_mapping=slot_mapping, k_pages=cache.k,
+                           v_pages=cache.v, k_block_scales=cache.k_block_scales,
+                           v_block_scales=cache.v_block_scales, k_scale=cache.k_scale,
+                           v_scale=cache.v_scale, q=q, inv_freq=inv_freq, interleaved=interleaved,
+                           q_out=o.get("q"), k_out=o.get("k"), v_out=o.get("v"), err=o["err"],
+                           stream=stream, prepare=prepare)
+    return c, o
+
+
+def append_kv(k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor, slot_mapping: torch.Tensor,
+              cache: KVCache, *, q: torch.Tensor | None = None, inv_freq: torch.Tensor | None = None,
+              interleaved: bool = False, want_values: bool = False, out=None, stream=None) -> dict:
+    """Keys (rotated to their positions when inv_freq is given) and values [T, heads, D] into the
+    cache at slot_mapping (a draft batch's, -1 skips the row).  Returns q (rotated, when given),
+    k and v (the values the cache now stands for, when want_values or given in out), err."""
+    return _append(k, v, positions, slot_mapping, cache, q, inv_freq, interleaved, want_values, out,
+                   stream, False)[1]
+
+
+def prepare_append_kv(k, v, positions, slot_mapping, cache, *, q=None, inv_freq=None,
+                      interleaved=False, want_values=False, out=None) -> tuple:
+    """The arguments of ``append_kv`` marshalled once: (call, outputs), call(stream=None)."""
+    return _append(k, v, positions, slot_mapping, cache, q, inv_freq, interleaved, want_values, out,
+                   None, True)
+
+
+def attend_workspace(device="cuda") -> torch.Tensor:
+    """Zero-initialised workspace of ``attend``, for any batch; one per stream."""
+    return torch.zeros(_b.pspec_attend_workspace_bytes(), dtype=torch.uint8, device=device)
+
+
+def _attend(q, cache, block_table, qsl, positions, seq_lens, scale, row_kind, want_lse, workspace,
+            out, stream, prepare):
+    o = dict(out) if out is not None else {}
+    if "out" not in o:
+        o["out"] = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if want_lse and "lse" not in o:
+        o["lse"] = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+    if "err" not in o:
+        o["err"] = _err(q.device)
+    ws = workspace if workspace is not None else attend_workspace(q.device)
+    c = _b.pspec_attend(q=q, k_pages=cache.k, v_pages=cache.v, k_block_scales=cache.k_block_scales,
+                        v_block_scales=cache.v_block_scales, k_scale=cache.k_scale,
+                        v_scale=cache.v_scale, block_table=block_table, qsl=qsl,
+                        positions=positions, seq_lens=seq_lens, row_kind=row_kind,
+                        scale=q.shape[-1] ** -0.5 if scale is None else scale, out=o["out"],
+                        lse=o.get("lse"), err=o["err"], workspace=ws, stream=stream, prepare=prepare)
+    return c, o
+
+
+def attend(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, qsl: torch.Tensor,
+           positions: torch.Tensor, seq_lens: torch.Tensor, *, scale: float | None = None,
+           row_kind: torch.Tensor | None = None, want_lse: bool = False,
+           workspace: torch.Tensor | None = None, out=None, stream=None) -> dict:
+    """Attention of the rows q [T, Hq, D] (sequence i's at qsl[i]..qsl[i+1], each at its position)
+    over a 4-bit cache; scale defaults to D^-0.5.  Returns out, err (+ lse)."""
+    return _attend(q, cache, block_table, qsl, positions, seq_lens, scale, row_kind, want_lse,
+                   workspace, out, stream, False)[1]
+
+
+def prepare_attend(q, cache, block_table, qsl, positions, seq_lens, *, scale=None, row_kind=None,
+                   want_lse=False, workspace=None, out=None) -> tuple:
+    """The arguments of ``attend`` marshalled once: (call, outputs), call(stream=None)."""
+    return _attend(q, cache, block_table, qsl, positions, seq_lens, scale, row_kind, want_lse,
+                   workspace, out, None, True)
+
+
+def _filtered(logits, uniforms, temperature, top_k, top_p, min_p, want_probs, out, stream, prepare):
+    o = dict(out) if out is not None else {}
+    shape, dev = tuple(logits.shape[:2]), logits.device
+    if "tokens" not in o:
+        o["tokens"] = torch.empty(shape, dtype=torch.int32, device=dev)
+    if want_probs and "probs" not in o:
+        o["probs"] = torch.empty(shape, dtype=torch.float32, device=dev)
+    if "err" not in o:
+        o["err"] = _err(dev)
+    c = _b.pspec_sample_filtered(logits=logits, uniforms=uniforms, temperature=temperature,
+                                 top_k=top_k, top_p=top_p, min_p=min_p, tokens=o["tokens"],
+                                 probs=o.get("probs"), err=o["err"], stream=stream, prepare=prepare)
+    return c, o
+
+
+def sample_filtered(logits: torch.Tensor, uniforms: torch.Tensor, *,
+                    temperature: torch.Tensor | None = None, top_k: torch.Tensor | None = None,
+                    top_p: torch.Tensor | None = None, min_p: torch.Tensor | None = None,
+                    want_probs: bool = False, out=None, stream=None) -> dict:
+    """Tokens drawn from logits [B, K, V] at uniforms [B, K] under each sequence's temperature,
+    top_k, top_p and min_p ([B] each, None: off).  Returns tokens, err (+ probs)."""
+    return _filtered(logits, uniforms, temperature, top_k, top_p, min_p, want_probs, out, stream,
+                     False)[1]
+
+
+def prepare_sample_filtered(logits, uniforms, *, temperature=None, top_k=None, top_p=None,
+                            min_p=None, want_probs=False, out=None) -> tuple:
+    """The arguments of ``sample_filtered`` marshalled once: (call, outputs), call(stream=None)."""
+    return _filtered(logits, uniforms, temperature, top_k, top_p, min_p, want_probs, out, None, True)

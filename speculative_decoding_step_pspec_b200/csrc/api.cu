@@ -47,6 +47,8 @@ bool dtype_ok(pspec_dtype d) { return d == PSPEC_F32 || d == PSPEC_BF16; }
 
 namespace pspec {
 
+void record_launches(int launches) { t_last_launches = launches; }
+
 pspec_status check_verify_host(const pspec_verify_args* a, bool rejection) {
   if (!a) return PSPEC_ERR_INVALID_ARG;
   if (a->B < 0 || a->K < 1 || a->V < 1 || a->ld < a->V) return PSPEC_ERR_INVALID_ARG;

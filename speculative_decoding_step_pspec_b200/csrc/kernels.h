@@ -128,4 +128,34 @@ cudaError_t launch_sample(const SampleLaunch& L, cudaStream_t stream);
 pspec_status check_verify_host(const pspec_verify_args* a, bool rejection);
 void record_last_call(int launches, int path);
 
+struct AppendLaunch {
+  pspec_append_args a;
+  int rows_per_cta;
+  long long slots;                // num_blocks * block_size
+  bool vec_q, vec_k, vec_v;       // rows whose four-element groups are aligned to their size
+  bool vec_qo, vec_ko, vec_vo;
+};
+cudaError_t launch_append(const AppendLaunch& L, cudaStream_t stream);
+
+struct AttendLaunch {
+  pspec_attend_args a;
+  int ctas;                       // persistent CTAs, at most kAttendMaxCtas
+  int* cnt;                       // [kAttendMaxCtas] arrivals of a tile that starts in a CTA
+  float* parts;                   // [2 * kAttendMaxCtas] partial tiles
+};
+cudaError_t launch_attend(const AttendLaunch& L, cudaStream_t stream);
+size_t attend_workspace_bytes();
+size_t attend_counter_bytes();    // the counters sit at the workspace's start
+
+struct FilterLaunch {
+  pspec_filter_args a;
+  int cluster;                    // CTAs per row
+  int chunks_per_cta;             // of 256 elements
+  int resident;                   // slices live in shared memory
+};
+cudaError_t launch_filter(const FilterLaunch& L, cudaStream_t stream);
+
+// pspec_last_launches of this host thread.
+void record_launches(int launches);
+
 }  // namespace pspec
