@@ -426,6 +426,35 @@ def test_sample_filtered_large_vocabulary(dtype, name):
     run_filtered(logits(5, B, K, V, dtype), uniforms(6, B, K), **kw)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("B,K,V", [(20, 2, 40001), (36, 1, 2050), (400, 4, 5003), (14, 3, 151936)])
+def test_sample_filtered_many_rows(B, K, V, dtype):
+    """Batches past the few rows whose slices live in shared memory, every request its own."""
+    g = np.random.default_rng(B + V)
+    x = logits(B + 1, B, K, V, dtype, pad=5)
+    x[:, :, 3::7] -= 4.0
+    for i in range(2):
+        kw = dict(t=g.choice([0.3, 0.8, 1.5, 3.0, 0.0], B), k=g.choice([0, 0, 1, 50, 900, 1500, V], B),
+                  p=g.choice([1.0, 0.3, 0.9, 0.99, 0.9999], B), m=g.choice([0.0, 0.0, 1e-6, 1e-3, 0.2, 1.0], B))
+        run_filtered(x, uniforms(B + V + i, B, K), **kw)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("B", [3, 40])
+@pytest.mark.parametrize("V", [9001, 70000])
+def test_sample_filtered_large_nuclei(V, B, dtype):
+    """Top-p sets of thousands of tokens, alone and beside a min-p that ends sooner, later or
+    about there, in rows of a narrow and a wide spread."""
+    x = logits(V + B, B, 1, V, dtype, sigma=2.0)
+    x[::2] *= 0.02
+    x[1::3] += 300.0
+    u = uniforms(V + B + 1, B, 1)
+    for p in (0.5, 0.9, 0.995):
+        run_filtered(x, u, p=[p] * B, t=[1.2] * B)
+        for m in (1e-9, 2e-4, 1e-2, 0.9):
+            run_filtered(x, u, p=[p] * B, t=[1.2] * B, m=[m] * B)
+
+
 def test_sample_filtered_past_the_shared_memory():
     """A vocabulary whose slices are read from global memory."""
     V = 1200000
