@@ -1,6 +1,6 @@
 // attend.cu -- attention of a ragged batch over the 4-bit paged cache (one launch).
 //
-// Work: a tile is up to 16 query rows (token x head of the group) of one sequence and kv head;
+// Work: a tile is 8, 16 or 32 query rows (token x head of the group) of one sequence and kv head;
 // its keys are cut into units of 64.  All units of all tiles form one list, dealt out evenly
 // to persistent CTAs, so ragged lengths cost no balance and neither grid nor workspace depends
 // on them.  A CTA's share covers at most two tiles partly (its first and its last); those go to
@@ -9,12 +9,15 @@
 //
 // Per unit each of the four warps takes 16 keys and keeps its own running maximum and sum, so
 // the loop has no barrier.  The cache's bytes come by asynchronous copies into a ring of the
-// warp's own.  A dot product may run over the head dimension in any order, and a sum over keys
-// in any order of keys, so the fragments of the fp16 tensor-core products are laid to the
-// cache's bytes instead of the other way round: a lane's 16 (or 8) bytes of one key ARE its
-// fragments of 8 (or 4) products, and two keys' nibbles interleaved are the pairs that the
-// product with the values wants.  Dequantised values are exact in fp16: 2 significant bits of
-// the code times 4 of the scale, between 2^-10 and 2688.
+// warp's own.  What costs is turning codes into fp16 (two conversions, two products and two
+// shuffles of bits for every four values), so the cache is the wide operand of the tensor-core
+// products -- 16 keys, or 16 of the values' columns, against 8 query rows -- and a converted
+// fragment serves every group of 8 rows in the tile; few rows waste half as much as with the
+// rows as the wide operand.  A dot product may run over the head dimension in any order, and a
+// sum over keys in any order of keys, so the fragments are laid to the cache's bytes: a lane's
+// 16 (or 8) bytes of one key ARE its fragments of 8 (or 4) products, and two keys' nibbles
+// interleaved are the pairs that the product with the values wants.  Dequantised values are
+// exact in fp16: 2 significant bits of the code times 4 of the scale, between 2^-10 and 2688.
 #include "common.cuh"
 #include "kernels.h"
 #include "plan.h"
@@ -27,26 +30,33 @@ constexpr int kAttWarps = 4;
 constexpr int kAttThreads = 32 * kAttWarps;
 constexpr int kStep = 16;                       // keys of one warp step
 constexpr int kUnit = kStep * kAttWarps;        // keys of one unit
-constexpr int kTileRows = 16;
 constexpr int kStages = 4;
-constexpr int kAttendMaxCtas = kNumSMs * 4;
+constexpr int kAttendMaxCtas = kNumSMs * 5;
 // Probabilities are formed as 2^(x - m + kShift) and the maximum m follows only when a row
 // passes it by more than kSlack: both leave them below 2^15 (fp16 holds 65504) and far above
 // fp16's subnormals, and the outputs are rescaled rarely.
 constexpr float kShift = 7.f, kSlack = 8.f;
+constexpr float kNoMax = -1e30f;                // taken from the exponents of a row without a key
+// Persistent CTAs that fit an SM by their registers.
+constexpr int attend_ctas_per_sm(int D, bool f32, int NT) {
+  return NT == 1 ? (D == 64 ? 5 : (f32 ? 3 : 4)) : (D == 64 && NT == 2 && !f32 ? 4 : (f32 ? 2 : 3));
+}
 
-template <int D>
+template <int D, int NT>
 struct Shape {
+  static constexpr int kRows = 8 * NT;          // rows of a tile
   static constexpr int kLane = D / 4;           // values of a key that a lane holds
   static constexpr int kWords = D / 32;         // their 32-bit words
   static constexpr int kK = D / 16;             // products over the head dimension
-  static constexpr int kCols = D / 8;           // output columns per column group
+  static constexpr int kM = D / 16;             // products over the output's columns
+  static constexpr int kCols = D / 8;           // output columns that a lane holds, contiguous
   static constexpr int kRow = D / 2;            // bytes of a key
   static constexpr int kScaleRow = D / 16;
   static constexpr int kStage = 2 * kStep * (kRow + kScaleRow);
   static constexpr int kRing = kStages * kStage;
-  static constexpr long long kPart = kTileRows * (D + 2);   // floats of a partial tile
+  static constexpr long long kPart = kRows * (D + 2);   // floats of a partial tile
 };
+constexpr long long kMaxPart = 32 * (64 + 2) > 16 * (128 + 2) ? 32 * (64 + 2) : 16 * (128 + 2);
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0));
@@ -60,6 +70,13 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
   asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Transposes an 8 x 8 matrix of 16-bit elements, two of a row in each lane.
+__device__ __forceinline__ uint32_t transpose8(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
 }
 
 // Four bytes of two e2m1 codes each, as four fp16 pairs (low nibble first).
@@ -107,6 +124,7 @@ struct Seq {
   int err;
 };
 
+template <int kTileRows>
 __device__ __forceinline__ Seq seq_of(const pspec_attend_args& a, int i, int group) {
   Seq s;
   s.err = 0;
@@ -166,14 +184,31 @@ __device__ __forceinline__ void store_out(uint16_t* p, float4 v) {
 }
 __device__ __forceinline__ void store_out(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
 
-template <int D, typename Tag>
+// Where a key lies: its page's column of the block table and its place in the page.
+struct Walk {
+  int col, off;
+  __device__ __forceinline__ void set(long long key, int block_size) {
+    col = (int)((unsigned)key / (unsigned)block_size);
+    off = (int)((unsigned)key - (unsigned)col * (unsigned)block_size);
+  }
+  __device__ __forceinline__ void advance(int cols, int rest, int block_size) {   // by a unit
+    col += cols;
+    off += rest;
+    if (off >= block_size) {
+      off -= block_size;
+      ++col;
+    }
+  }
+};
+
+template <int D, int NT>
 struct AttendSmem {
   union {
-    alignas(128) uint8_t ring[kAttWarps][Shape<D>::kRing];
-    float out[kAttWarps][kTileRows][D + 4];
+    alignas(128) uint8_t ring[kAttWarps][Shape<D, NT>::kRing];
+    float out[kAttWarps][Shape<D, NT>::kRows][D + 4];
   };
-  float m[kAttWarps][kTileRows];
-  float l[kAttWarps][kTileRows];
+  float m[kAttWarps][Shape<D, NT>::kRows];
+  float l[kAttWarps][Shape<D, NT>::kRows];
   unsigned live[kAttWarps][kStages];          // which of the stage's keys exist
   long long scan[kAttWarps];
   int start_seq;
@@ -181,14 +216,15 @@ struct AttendSmem {
   int last;
 };
 
-template <int D, typename Tag, bool kWholePages>
-__global__ void __launch_bounds__(kAttThreads, sizeof(typename Tag::elem) == 2 ? 3 : 2)
+template <int D, typename Tag, bool kWholePages, int NT>
+__global__ void __launch_bounds__(kAttThreads, attend_ctas_per_sm(D, sizeof(typename Tag::elem) == 4, NT))
 attend_kernel(const AttendLaunch L) {
   using elem = typename Tag::elem;
-  using S = Shape<D>;
+  using S = Shape<D, NT>;
+  constexpr int kTileRows = S::kRows;
   constexpr bool kF32 = sizeof(elem) == 4;     // two fp16 terms for queries and probabilities
   extern __shared__ __align__(128) uint8_t s_raw[];
-  auto& sm = *reinterpret_cast<AttendSmem<D, Tag>*>(s_raw);
+  auto& sm = *reinterpret_cast<AttendSmem<D, NT>*>(s_raw);
   const pspec_attend_args& a = L.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
@@ -201,7 +237,7 @@ attend_kernel(const AttendLaunch L) {
   long long mine = 0;
   int bits = 0;
   for (int i = i_lo; i < i_hi; ++i) {
-    const Seq s = seq_of(a, i, group);
+    const Seq s = seq_of<kTileRows>(a, i, group);
     mine += s.units * s.tiles * a.Hkv;
     bits |= s.err;
   }
@@ -226,7 +262,7 @@ attend_kernel(const AttendLaunch L) {
     long long at = base + incl - mine;
     if (w0 >= at && w0 < at + mine) {
       for (int i = i_lo; i < i_hi; ++i) {
-        const Seq s = seq_of(a, i, group);
+        const Seq s = seq_of<kTileRows>(a, i, group);
         const long long n = s.units * s.tiles * a.Hkv;
         if (w0 < at + n) {
           sm.start_seq = i;
@@ -243,18 +279,23 @@ attend_kernel(const AttendLaunch L) {
 
   const uint32_t ring = (uint32_t)__cvta_generic_to_shared(sm.ring[warp]);
   const uint8_t* ring_p = sm.ring[warp];
-  // shared-memory offsets of the lane's bytes: key tau of tile j is 8 j + (g even ? g/2 :
-  // 7 - g/2), so that the keys of a lane's value pairs are t, 7-t, 8+t and 15-t; 16-byte
-  // chunks of odd key pairs are swapped by two (D = 128) to keep the reads free of conflicts
+  // Row r of a product's 16 keys is key r/2 (r even) or 7 - r/2 (odd) of the lower or upper
+  // eight, so that the keys of a lane's value pairs are t, 7-t, 8+t and 15-t; 16-byte chunks of
+  // odd key pairs are swapped by two (D = 128) to keep the reads free of conflicts.
   const int tau = (g & 1) ? 7 - (g >> 1) : g >> 1;
+  constexpr int kWalks = kWholePages ? 1 : (D == 128 ? 3 : 2);
+  const int walk_key[3] = {kWholePages ? 0 : (D == 128 ? lane >> 2 : lane >> 1),
+                           D == 128 ? (lane >> 2) + 8 : lane & 15, lane & 15};
+
+  const int unit_cols = kUnit / a.block_size, unit_rest = kUnit - unit_cols * a.block_size;
 
   long long w = w0;
   bool first = true;
-  Seq s = seq_of(a, seq, group);
+  Seq s = seq_of<kTileRows>(a, seq, group);
   while (w < w1) {
     while (w >= prefix + s.units * s.tiles * a.Hkv) {
       prefix += s.units * s.tiles * a.Hkv;
-      s = seq_of(a, ++seq, group);
+      s = seq_of<kTileRows>(a, ++seq, group);
     }
     const long long item = (w - prefix) / s.units;
     const long long item0 = prefix + item * s.units;          // the tile's first unit
@@ -264,89 +305,101 @@ attend_kernel(const AttendLaunch L) {
     const long long u1 = min(s.units, w1 - item0);
     w = item0 + u1;
 
-    const RowRef ra = row_of(a, s, group, h, r0 + g), rb = row_of(a, s, group, h, r0 + g + 8);
-    int lim_hi = max(ra.limit, rb.limit);
-    int lim_lo = min(ra.limit < 0 ? 0x7fffffff : ra.limit, rb.limit < 0 ? 0x7fffffff : rb.limit);
-#pragma unroll
-    for (int o = 4; o < 32; o <<= 1) {
-      lim_hi = max(lim_hi, __shfl_xor_sync(0xffffffffu, lim_hi, o));
-      lim_lo = min(lim_lo, __shfl_xor_sync(0xffffffffu, lim_lo, o));
-    }
+    // the keys that the tile's rows may see: lane r < kTileRows looks at row r
+    const RowRef rr = row_of(a, s, group, h, lane < kTileRows ? r0 + lane : (long long)s.rows * group);
+    int lim_hi = rr.limit, lim_lo = rr.limit < 0 ? 0x7fffffff : rr.limit;
+    lim_hi = __reduce_max_sync(0xffffffffu, lim_hi);
+    lim_lo = __reduce_min_sync(0xffffffffu, lim_lo);
     const int* table = a.block_table + (long long)seq * a.max_blocks;
     const int steps = (int)(min(u1, ((long long)max(lim_hi, 0) + kUnit - 1) / kUnit) - u0);
 
-    // ---- one step's copies; `blk` is the page of a step inside one page
-    auto block_of = [&](long long key) -> int {
-      return key < s.len ? __ldg(table + (unsigned)key / (unsigned)a.block_size) : -1;
-    };
-    auto issue = [&](int step, int blk) {
-      const long long k0 = (u0 + step) * kUnit + warp * kStep;
-      const uint32_t dst = ring + (step % kStages) * S::kStage;
-      auto row_at = [&](int key, bool& live) -> long long {     // row of the cache
-        const long long k = k0 + key;
-        int b = blk;
-        if constexpr (!kWholePages) b = block_of(k);
-        live = k < s.len && b >= 0 && b < a.num_blocks;
-        if (!live) return 0;
-        return ((long long)b * a.Hkv + h) * a.block_size + (int)((unsigned)k % (unsigned)a.block_size);
-      };
-      bool live;
-      if constexpr (D == 128) {
+    // ---- one step's copies, the pages looked up a step ahead
+    const long long key0 = u0 * kUnit + warp * kStep;         // of step 0
+    Walk walk[kWalks];
+    int blk[kWalks];
+    auto look = [&](int step) {
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const int key = (lane >> 2) + 8 * half, c = lane & 3;
-          const long long row = row_at(key, live) * S::kRow + c * 16;
-          const uint32_t to = dst + key * S::kRow + ((c ^ ((key >> 1 & 1) << 1)) << 4);
-          cp_async16(to, static_cast<const uint8_t*>(a.k_pages) + row, live);
-          cp_async16(to + kStep * S::kRow, static_cast<const uint8_t*>(a.v_pages) + row, live);
-        }
-      } else {
-        const int key = lane >> 1, c = lane & 1;
-        const long long row = row_at(key, live) * S::kRow + c * 16;
-        const uint32_t to = dst + key * S::kRow + (c << 4);
-        cp_async16(to, static_cast<const uint8_t*>(a.k_pages) + row, live);
-        cp_async16(to + kStep * S::kRow, static_cast<const uint8_t*>(a.v_pages) + row, live);
+      for (int i = 0; i < kWalks; ++i)
+        blk[i] = key0 + (long long)step * kUnit + walk_key[i] < s.len ? __ldg(table + walk[i].col) : -1;
+    };
+#pragma unroll
+    for (int i = 0; i < kWalks; ++i) walk[i].set(key0 + walk_key[i], a.block_size);
+    look(0);
+    auto issue = [&](int step) {
+      const int left = (int)max(0LL, min((long long)kStep, (long long)s.len - key0 - (long long)step * kUnit));
+      const uint32_t dst = ring + (step % kStages) * S::kStage;
+      long long row[kWalks];
+      bool live[kWalks];
+#pragma unroll
+      for (int i = 0; i < kWalks; ++i) {
+        live[i] = (unsigned)blk[i] < (unsigned)a.num_blocks;
+        row[i] = live[i] ? ((long long)blk[i] * a.Hkv + h) * a.block_size + walk[i].off : 0;
+        walk[i].advance(unit_cols, unit_rest, a.block_size);
       }
-      const int key = lane & 15;
-      const long long row = row_at(key, live) * S::kScaleRow;
-      const void* src = static_cast<const uint8_t*>(lane < 16 ? a.k_block_scales : a.v_block_scales) + row;
-      cp_async_small<S::kScaleRow>(dst + 2 * kStep * S::kRow + lane * S::kScaleRow, src, live);
-      const unsigned alive = __ballot_sync(0xffffffffu, live) & 0xffffu;
+      look(step + 1);
+      auto copies = [&](int key, int c, long long r, bool ok) {
+        const long long at = r * S::kRow + c * 16;
+        const uint32_t to = dst + key * S::kRow + (D == 128 ? (c ^ ((key >> 1 & 1) << 1)) << 4 : c << 4);
+        cp_async16(to, static_cast<const uint8_t*>(a.k_pages) + at, ok);
+        cp_async16(to + kStep * S::kRow, static_cast<const uint8_t*>(a.v_pages) + at, ok);
+      };
+      const int skey = lane & 15;
+      bool ok;
+      long long srow;
+      if constexpr (kWholePages) {
+        if constexpr (D == 128) {
+          const int key = lane >> 2;
+          copies(key, lane & 3, live[0] && key < left ? row[0] + key : 0, live[0] && key < left);
+          copies(key + 8, lane & 3, live[0] && key + 8 < left ? row[0] + key + 8 : 0, live[0] && key + 8 < left);
+        } else {
+          const int key = lane >> 1;
+          copies(key, lane & 1, live[0] && key < left ? row[0] + key : 0, live[0] && key < left);
+        }
+        ok = live[0] && skey < left;
+        srow = ok ? row[0] + skey : 0;
+      } else {
+        if constexpr (D == 128) {
+          copies(lane >> 2, lane & 3, row[0], live[0]);
+          copies((lane >> 2) + 8, lane & 3, row[1], live[1]);
+        } else {
+          copies(lane >> 1, lane & 1, row[0], live[0]);
+        }
+        ok = live[kWalks - 1];
+        srow = row[kWalks - 1];
+      }
+      const uint8_t* src = static_cast<const uint8_t*>(lane < 16 ? a.k_block_scales : a.v_block_scales) + srow * S::kScaleRow;
+      cp_async_small<S::kScaleRow>(dst + 2 * kStep * S::kRow + lane * S::kScaleRow, src, ok);
+      const unsigned alive = __ballot_sync(0xffffffffu, ok) & 0xffffu;
       if (lane == 0) {
         sm.live[warp][step % kStages] = alive;
         // a key that exists but whose page does not is hidden
-        const int there = (int)max(0LL, min((long long)kStep, s.len - k0));
-        if (alive != (1u << there) - 1u) set_err(a.err, PSPEC_DEVERR_BLOCK_RANGE);
+        if (alive != (1u << left) - 1u) set_err(a.err, PSPEC_DEVERR_BLOCK_RANGE);
       }
     };
-    int next_blk = -1;
-    if (kWholePages) next_blk = block_of(u0 * kUnit + warp * kStep);
     auto issue_next = [&](int step) {
-      if (step < steps) {
-        const int blk = next_blk;
-        if (kWholePages) next_blk = block_of((u0 + step + 1) * kUnit + warp * kStep);
-        issue(step, blk);
-      }
+      if (step < steps) issue(step);
       asm volatile("cp.async.commit_group;");
     };
     for (int st = 0; st < kStages - 1; ++st) issue_next(st);
 
-    // ---- the query rows as fragments: power-of-two scaled into fp16's range
-    uint32_t qa[S::kK][4], ql[kF32 ? S::kK : 1][4];
-    float mult[2];
+    // ---- the query rows as fragments: lane (g, t) has a quarter of row 8n + g, power-of-two
+    // scaled into fp16's range
+    uint32_t qb[NT][S::kK][2], ql[kF32 ? NT : 1][S::kK][2];
+    float mult[NT][2];                          // of rows 8n + 2t and 8n + 2t + 1
+    int limit[NT][2];
     {
       const float ks = a.k_scale ? __ldg(a.k_scale + h) : 1.f;
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const RowRef& rr = half ? rb : ra;
+      for (int n = 0; n < NT; ++n) {
+        const RowRef rq = row_of(a, s, group, h, r0 + 8 * n + g);
         float x[S::kLane];
         float top = 0.f;
-        const long long tok = rr.at / a.Hq;
-        const elem* p = static_cast<const elem*>(a.q) + tok * a.q_stride + (rr.at - tok * a.Hq) * D + t * S::kLane;
+        const long long tok = rq.at / a.Hq;
+        const elem* p = static_cast<const elem*>(a.q) + tok * a.q_stride + (rq.at - tok * a.Hq) * D + t * S::kLane;
 #pragma unroll
         for (int j = 0; j < S::kLane; j += 2) {
           x[j] = x[j + 1] = 0.f;
-          if (rr.limit > 0) load_q2(p + j, x[j], x[j + 1]);
+          if (rq.limit > 0) load_q2(p + j, x[j], x[j + 1]);
           top = fmaxf(top, fmaxf(fabsf(x[j]), fabsf(x[j + 1])));
         }
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
@@ -355,25 +408,40 @@ attend_kernel(const AttendLaunch L) {
         const int ex = (int)(__float_as_uint(top) >> 23) - 127;
         const int up = top == 0.f || ex == 128 ? 0 : min(100, 14 - ex);
         const float f = __uint_as_float((unsigned)(127 + up) << 23);
-        mult[half] = a.scale * kLog2e * ks * __uint_as_float((unsigned)(127 - up) << 23);
+        const float back = a.scale * kLog2e * ks * __uint_as_float((unsigned)(127 - up) << 23);
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          mult[n][r] = __shfl_sync(0xffffffffu, back, (2 * t + r) * 4);
+          limit[n][r] = __shfl_sync(0xffffffffu, rq.limit, (2 * t + r) * 4);
+        }
 #pragma unroll
         for (int k = 0; k < S::kK; ++k)
 #pragma unroll
           for (int pair = 0; pair < 2; ++pair) {
             const float u = x[4 * k + 2 * pair] * f, v = x[4 * k + 2 * pair + 1] * f;
             const uint32_t hi = pack_half(u, v);
-            qa[k][2 * pair + half] = hi;
-            if constexpr (kF32) ql[k][2 * pair + half] = pack_half(u - half_lo(hi), v - half_hi(hi));
+            qb[n][k][pair] = hi;
+            if constexpr (kF32) ql[n][k][pair] = pack_half(u - half_lo(hi), v - half_hi(hi));
           }
       }
     }
 
-    float o[S::kCols][4];
+    // o[n][m]: rows 8n + 2t (elements 0, 2) and 8n + 2t + 1 (1, 3), columns kCols g + 2m, + 1
+    float o[NT][S::kM][4];
+    float m[NT][2], at[NT][2], l[NT][2];        // at: what is taken from the exponents
 #pragma unroll
-    for (int j = 0; j < S::kCols; ++j)
+    for (int n = 0; n < NT; ++n) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) o[j][c] = 0.f;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+      for (int j = 0; j < S::kM; ++j)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) o[n][j][c] = 0.f;
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        m[n][r] = -INFINITY;
+        at[n][r] = kNoMax;
+        l[n][r] = 0.f;
+      }
+    }
 
     for (int step = 0; step < steps; ++step) {
       issue_next(step + kStages - 1);
@@ -383,93 +451,112 @@ attend_kernel(const AttendLaunch L) {
       const long long k0 = (u0 + step) * kUnit + warp * kStep;
       const unsigned alive = sm.live[warp][step % kStages];
 
-      // ---- scores: 16 rows x 16 keys
-      float sc[2][4] = {};
+      // ---- scores: 16 keys x 8 NT rows
+      float sc[NT][4] = {};
+      {
+        uint32_t wd[2][S::kWords], f[2][2];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int key = 8 * j + tau;
-        uint32_t wd[S::kWords];
-        if constexpr (D == 128) {
-          const uint4 v = *reinterpret_cast<const uint4*>(buf + key * S::kRow + ((t ^ ((key >> 1 & 1) << 1)) << 4));
-          wd[0] = v.x; wd[1] = v.y; wd[2] = v.z; wd[3] = v.w;
-        } else {
-          const uint2 v = *reinterpret_cast<const uint2*>(buf + key * S::kRow + t * 8);
-          wd[0] = v.x; wd[1] = v.y;
-        }
-        const uint8_t* sp = buf + 2 * kStep * S::kRow + key * S::kScaleRow;
-        uint32_t s_lo, s_hi;
-        if constexpr (D == 128) {
-          const uint32_t two = scales_to_half(*reinterpret_cast<const uint16_t*>(sp + 2 * t));
-          s_lo = __byte_perm(two, 0, 0x1010);
-          s_hi = __byte_perm(two, 0, 0x3232);
-        } else {
-          const uint32_t one = sp[t];
-          s_lo = s_hi = scales_to_half(one | one << 8);
+        for (int j = 0; j < 2; ++j) {
+          const int key = 8 * j + tau;
+          if constexpr (D == 128) {
+            const uint4 v = *reinterpret_cast<const uint4*>(buf + key * S::kRow + ((t ^ ((key >> 1 & 1) << 1)) << 4));
+            wd[j][0] = v.x; wd[j][1] = v.y; wd[j][2] = v.z; wd[j][3] = v.w;
+          } else {
+            const uint2 v = *reinterpret_cast<const uint2*>(buf + key * S::kRow + t * 8);
+            wd[j][0] = v.x; wd[j][1] = v.y;
+          }
+          const uint8_t* sp = buf + 2 * kStep * S::kRow + key * S::kScaleRow;
+          if constexpr (D == 128) {
+            const uint32_t two = scales_to_half(*reinterpret_cast<const uint16_t*>(sp + 2 * t));
+            f[j][0] = __byte_perm(two, 0, 0x1010);
+            f[j][1] = __byte_perm(two, 0, 0x3232);
+          } else {
+            const uint32_t one = sp[t];
+            f[j][0] = f[j][1] = scales_to_half(one | one << 8);
+          }
         }
 #pragma unroll
         for (int k = 0; k < S::kWords; ++k) {
-          uint32_t b[4];
-          codes_to_half(wd[k], b);
-          const uint32_t f = 2 * k < S::kWords ? s_lo : s_hi;
+          uint32_t x[2][4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) b[i] = hmul2(b[i], f);
-          mma16816(sc[j], qa[2 * k], b[0], b[1]);
-          mma16816(sc[j], qa[2 * k + 1], b[2], b[3]);
-          if constexpr (kF32) {
-            mma16816(sc[j], ql[2 * k], b[0], b[1]);
-            mma16816(sc[j], ql[2 * k + 1], b[2], b[3]);
+          for (int j = 0; j < 2; ++j) {
+            codes_to_half(wd[j][k], x[j]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[j][i] = hmul2(x[j][i], f[j][2 * k < S::kWords ? 0 : 1]);
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t fr[4] = {x[0][2 * i], x[1][2 * i], x[0][2 * i + 1], x[1][2 * i + 1]};
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              mma16816(sc[n], fr, qb[n][2 * k + i][0], qb[n][2 * k + i][1]);
+              if constexpr (kF32) mma16816(sc[n], fr, ql[n][2 * k + i][0], ql[n][2 * k + i][1]);
+            }
           }
         }
       }
 
-      // ---- softmax in base 2; a lane's columns of tile j are keys 8j + t and 8j + 7 - t
+      // ---- softmax in base 2: exponents less what each row takes; the maximum is looked for only
+      // when one of them passes the slack
+      const bool masked = alive != 0xffffu || k0 + kStep > lim_lo;
+      auto exponents = [&](float (&y)[NT][4]) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) sc[j][c] *= mult[c >> 1];
-      if (alive != 0xffffu || k0 + kStep > lim_lo) {
+          for (int c = 0; c < 4; ++c) y[n][c] = fmaf(sc[n][c], mult[n][c & 1], -at[n][c & 1]);
+        if (masked) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+          for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int key = 8 * j + ((c & 1) ? 7 - t : t);
-            if (!(alive >> key & 1) || k0 + key >= (c >> 1 ? rb.limit : ra.limit)) sc[j][c] = -INFINITY;
-          }
-      }
-      float top[2];
+            for (int c = 0; c < 4; ++c) {
+              const int key = (c & 2 ? 8 : 0) + tau;
+              if (!(alive >> key & 1) || k0 + key >= limit[n][c & 1]) y[n][c] = -INFINITY;
+            }
+        }
+      };
+      float y[NT][4];
+      exponents(y);
       bool grow = false;
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        top[r] = fmaxf(fmaxf(sc[0][2 * r], sc[0][2 * r + 1]), fmaxf(sc[1][2 * r], sc[1][2 * r + 1]));
-        top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
-        top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
-        grow |= top[r] > m[r] + kSlack;
-      }
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) grow |= y[n][c] > kShift + kSlack;
       if (__any_sync(0xffffffffu, grow)) {
-        float f[2];
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const float n = fmaxf(m[r], top[r]);
-          f[r] = n == -INFINITY ? 1.f : ex2(m[r] - n);
-          m[r] = n;
-          l[r] *= f[r];
-        }
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int j = 0; j < S::kCols; ++j)
+          for (int r = 0; r < 2; ++r) {
+            float top = -INFINITY;
+            if (y[n][r] > -INFINITY) top = sc[n][r] * mult[n][r];
+            if (y[n][r + 2] > -INFINITY) top = fmaxf(top, sc[n][r + 2] * mult[n][r]);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) o[j][c] *= f[c >> 1];
+            for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+            const float old = m[n][r];
+            m[n][r] = fmaxf(old, top);
+            if (m[n][r] > old) {
+              const float f = ex2(old - m[n][r]);
+              at[n][r] = m[n][r] - kShift;
+              l[n][r] *= f;
+#pragma unroll
+              for (int j = 0; j < S::kM; ++j) {
+                o[n][j][r] *= f;
+                o[n][j][r + 2] *= f;
+              }
+            }
+          }
+        exponents(y);
       }
-      uint32_t pa[4], pl[4];
+      uint32_t pb[NT][2], pl[kF32 ? NT : 1][2];
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const float at = m[r] == -INFINITY ? 0.f : m[r] - kShift;
-          const float x = ex2(sc[j][2 * r] - at), y = ex2(sc[j][2 * r + 1] - at);
-          l[r] += x + y;
-          const uint32_t hi = pack_half(x, y);
-          pa[2 * j + r] = hi;
-          if constexpr (kF32) pl[2 * j + r] = pack_half(x - half_lo(hi), y - half_hi(hi));
+        for (int j = 0; j < 2; ++j) {
+          const float u = ex2(y[n][2 * j]), v = ex2(y[n][2 * j + 1]);
+          l[n][0] += u;
+          l[n][1] += v;
+          const uint32_t hi = pack_half(u, v);
+          pb[n][j] = transpose8(hi);
+          if constexpr (kF32) pl[n][j] = transpose8(pack_half(u - half_lo(hi), v - half_hi(hi)));
         }
 
       // ---- outputs: pairs of keys (t, 7 - t) and (8 + t, 15 - t)
@@ -498,24 +585,26 @@ attend_kernel(const AttendLaunch L) {
       }
 #pragma unroll
       for (int k = 0; k < D / 64; ++k) {
+        uint32_t fr[4][4];                                  // of 4 products: even, odd columns of
+#pragma unroll                                              // the first pair of keys, of the second
+        for (int pr = 0; pr < 2; ++pr)
 #pragma unroll
-        for (int odd = 0; odd < 2; ++odd) {                 // even, then odd columns of the word
-          uint32_t b0[4], b1[4];
-#pragma unroll
-          for (int pr = 0; pr < 2; ++pr) {
+          for (int odd = 0; odd < 2; ++odd) {
             const uint32_t x = vw[2 * pr][k], y = vw[2 * pr + 1][k];
             const uint32_t both = odd ? ((x >> 4) & 0x0f0f0f0fu) | (y & 0xf0f0f0f0u)
                                       : (x & 0x0f0f0f0fu) | ((y << 4) & 0xf0f0f0f0u);
-            if (pr == 0) codes_to_half(both, b0);
-            else codes_to_half(both, b1);
+            uint32_t b[4];
+            codes_to_half(both, b);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) fr[i][2 * pr + odd] = hmul2(b[i], f[pr]);
           }
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t x = hmul2(b0[i], f[0]), y = hmul2(b1[i], f[1]);
-            mma16816(o[8 * k + 2 * i + odd], pa, x, y);
-            if constexpr (kF32) mma16816(o[8 * k + 2 * i + odd], pl, x, y);
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            mma16816(o[n][4 * k + i], fr[i], pb[n][0], pb[n][1]);
+            if constexpr (kF32) mma16816(o[n][4 * k + i], fr[i], pl[n][0], pl[n][1]);
           }
-        }
       }
       __syncwarp();                                         // the stage may be refilled
     }
@@ -524,21 +613,21 @@ attend_kernel(const AttendLaunch L) {
 
     // ---- the four warps' results joined
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-      const int row = g + 8 * r;
-      if (t == 0) {
-        sm.m[warp][row] = m[r];
-        sm.l[warp][row] = l[r];
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) l[n][r] += __shfl_xor_sync(0xffffffffu, l[n][r], x);
+        const int row = 8 * n + 2 * t + r;
+        if (g == 0) {
+          sm.m[warp][row] = m[n][r];
+          sm.l[warp][row] = l[n][r];
+        }
+#pragma unroll
+        for (int j = 0; j < S::kM; j += 2)
+          *reinterpret_cast<float4*>(&sm.out[warp][row][S::kCols * g + 2 * j]) =
+              make_float4(o[n][j][r], o[n][j][r + 2], o[n][j + 1][r], o[n][j + 1][r + 2]);
       }
-#pragma unroll
-      for (int n = 0; n < 2; ++n)                           // column group 2t + n
-#pragma unroll
-        for (int j = 0; j < S::kCols; j += 4)
-          *reinterpret_cast<float4*>(&sm.out[warp][row][S::kCols * (2 * t + n) + j]) =
-              make_float4(o[j][2 * r + n], o[j + 1][2 * r + n], o[j + 2][2 * r + n], o[j + 3][2 * r + n]);
-    }
     __syncthreads();
     const bool whole = u0 == 0 && u1 == s.units;
     float* part = L.parts + (2LL * cta + (first ? 0 : 1)) * S::kPart;
@@ -594,26 +683,59 @@ attend_kernel(const AttendLaunch L) {
         __threadfence();
         // in CTA a the tile is the first of the share only when it begins there
         const long long slot_a = 2 * cta_a + (cta_a * U / E == item0 ? 0 : 1);
-        for (int i = tid; i < kTileRows * (D / 4); i += kAttThreads) {
-          const int row = i / (D / 4), d = (i - row * (D / 4)) * 4;
-          const RowRef rr = row_of(a, s, group, h, r0 + row);
-          if (rr.limit < 0) continue;
-          float M = -INFINITY;
-          for (long long c = cta_a; c <= cta_b; ++c) {
-            const float* p = L.parts + (c == cta_a ? slot_a : 2 * c) * S::kPart;
-            M = fmaxf(M, ld_cg(p + kTileRows * D + row));
-          }
-          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-          float sum = 0.f;
-          for (long long c = cta_a; c <= cta_b; ++c) {
-            const float* p = L.parts + (c == cta_a ? slot_a : 2 * c) * S::kPart;
-            const float mc = ld_cg(p + kTileRows * D + row);
+        auto part_of = [&](long long c) { return L.parts + (c == cta_a ? slot_a : 2 * c) * S::kPart; };
+        const int n = (int)(cta_b - cta_a) + 1;
+        constexpr int kSeats = kAttThreads / kTileRows;     // threads of a row
+        constexpr int kBatch = 32;                          // parts whose factors are held at once
+        constexpr int kHeld = kTileRows * (D / 4) / kAttThreads;
+        float* seat = reinterpret_cast<float*>(s_raw);      // [kSeats][rows], then [rows]
+        float* factor = seat + kAttThreads + kTileRows;     // [kBatch][rows]
+        const int row = tid % kTileRows, place = tid / kTileRows;
+        float M = -INFINITY;
+#pragma unroll 4
+        for (int c = place; c < n; c += kSeats) M = fmaxf(M, ld_cg(part_of(cta_a + c) + kTileRows * D + row));
+        seat[tid] = M;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kSeats; ++i) M = fmaxf(M, seat[i * kTileRows + row]);
+        float sum = 0.f;
+        float4 v[kHeld];
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int c0 = 0; c0 < n; c0 += kBatch) {
+          const int nb = min(kBatch, n - c0);
+          __syncthreads();
+#pragma unroll 4
+          for (int c = place; c < nb; c += kSeats) {
+            const float* p = part_of(cta_a + c0 + c) + kTileRows * D + row;
+            const float mc = ld_cg(p), lc = ld_cg(p + kTileRows);
             const float f = mc == -INFINITY ? 0.f : ex2(mc - M);
-            const float4 x = ld_cg(reinterpret_cast<const float4*>(p + row * D + d));
-            sum += f * ld_cg(p + kTileRows * D + kTileRows + row);
-            v.x += f * x.x; v.y += f * x.y; v.z += f * x.z; v.w += f * x.w;
+            factor[c * kTileRows + row] = f;
+            sum += f * lc;
           }
-          finish(rr, d, M, sum, v);
+          __syncthreads();
+#pragma unroll
+          for (int i = 0; i < kHeld; ++i) {
+            const int at = i * kAttThreads + tid, r = at / (D / 4);
+#pragma unroll 8
+            for (int c = 0; c < nb; ++c) {
+              const float4 x = ld_cg(reinterpret_cast<const float4*>(part_of(cta_a + c0 + c)) + at);
+              const float f = factor[c * kTileRows + r];
+              v[i].x += f * x.x; v[i].y += f * x.y; v[i].z += f * x.z; v[i].w += f * x.w;
+            }
+          }
+        }
+        __syncthreads();
+        seat[tid] = sum;
+        if (place == 0) factor[row] = M;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) {
+          const int at = i * kAttThreads + tid, r = at / (D / 4);
+          float total = 0.f;
+#pragma unroll
+          for (int x = 0; x < kSeats; ++x) total += seat[x * kTileRows + r];
+          finish(row_of(a, s, group, h, r0 + r), (at - r * (D / 4)) * 4, factor[r], total, v[i]);
         }
       }
     }
@@ -621,26 +743,36 @@ attend_kernel(const AttendLaunch L) {
   }
 }
 
-template <int D, typename Tag>
-cudaError_t launch_d(const AttendLaunch& L, cudaStream_t stream) {
-  constexpr int smem = sizeof(AttendSmem<D, Tag>);
-  const bool whole = L.a.block_size % kStep == 0;
-  auto* fn = whole ? attend_kernel<D, Tag, true> : attend_kernel<D, Tag, false>;
-  static_assert(smem <= 48 * 1024, "within the default limit");
+template <int D, typename Tag, int NT>
+cudaError_t launch_nt(AttendLaunch L, cudaStream_t stream) {
+  constexpr int smem = sizeof(AttendSmem<D, NT>);
+  constexpr int ctas = attend_ctas_per_sm(D, sizeof(typename Tag::elem) == 4, NT);
+  static_assert(smem <= 48 * 1024 && smem * ctas <= 220 * 1024, "within the default limit, and all fit");
+  static_assert(Shape<D, NT>::kPart <= kMaxPart && ctas * kNumSMs <= kAttendMaxCtas, "within the workspace");
+  L.ctas = kNumSMs * ctas;
+  auto* fn = L.a.block_size % kStep == 0 ? attend_kernel<D, Tag, true, NT> : attend_kernel<D, Tag, false, NT>;
   fn<<<L.ctas, kAttThreads, smem, stream>>>(L);
   return cudaGetLastError();
+}
+
+// Tiles for the rows that a sequence has on average.
+template <int D, typename Tag>
+cudaError_t launch_d(const AttendLaunch& L, cudaStream_t stream) {
+  const long long rows = ((long long)L.a.T * (L.a.Hq / L.a.Hkv) + L.a.B - 1) / L.a.B;
+  constexpr int most = D == 64 && sizeof(typename Tag::elem) == 2 ? 4 : 2;
+  if (rows <= 8) return launch_nt<D, Tag, 1>(L, stream);
+  if (rows <= 16 || most == 2) return launch_nt<D, Tag, 2>(L, stream);
+  return launch_nt<D, Tag, most>(L, stream);
 }
 
 }  // namespace
 
 size_t attend_counter_bytes() { return (sizeof(int) * kAttendMaxCtas + 255) / 256 * 256; }
 size_t attend_workspace_bytes() {
-  return attend_counter_bytes() + sizeof(float) * 2 * kAttendMaxCtas * Shape<128>::kPart;
+  return (attend_counter_bytes() + sizeof(float) * 2 * kAttendMaxCtas * kMaxPart + 255) / 256 * 256;
 }
 
-cudaError_t launch_attend(const AttendLaunch& in, cudaStream_t stream) {
-  AttendLaunch L = in;
-  L.ctas = kNumSMs * (L.a.dtype == PSPEC_BF16 ? 3 : 2);
+cudaError_t launch_attend(const AttendLaunch& L, cudaStream_t stream) {
   if (L.a.dtype == PSPEC_BF16)
     return L.a.D == 64 ? launch_d<64, BF16Tag>(L, stream) : launch_d<128, BF16Tag>(L, stream);
   return L.a.D == 64 ? launch_d<64, F32Tag>(L, stream) : launch_d<128, F32Tag>(L, stream);
