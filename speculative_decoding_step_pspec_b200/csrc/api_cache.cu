@@ -88,14 +88,13 @@ pspec_status pspec_append_kv(const pspec_append_args* a, cudaStream_t stream) {
   AppendLaunch L{};
   L.a = *a;
   L.slots = slots;
-  const long long w = 4 * e;                          // a thread's four elements
-  L.vec_q = a->q && aligned(a->q, w) && a->q_stride % 4 == 0;
-  L.vec_k = aligned(a->k, w) && a->k_stride % 4 == 0;
-  L.vec_v = aligned(a->v, w) && a->v_stride % 4 == 0;
-  L.vec_qo = a->q && aligned(a->q_out, w);
-  L.vec_ko = aligned(a->k_out, w);
-  L.vec_vo = aligned(a->v_out, w);
-  L.rows_per_cta = 1;
+  // eight elements of a head at a time, in 16-byte pieces
+  L.vec_q = a->q && aligned(a->q, 16) && a->q_stride * e % 16 == 0;
+  L.vec_k = aligned(a->k, 16) && a->k_stride * e % 16 == 0;
+  L.vec_v = aligned(a->v, 16) && a->v_stride * e % 16 == 0;
+  L.vec_qo = a->q && aligned(a->q_out, 16);
+  L.vec_ko = aligned(a->k_out, 16);
+  L.vec_vo = aligned(a->v_out, 16);
   if (launch_append(L, stream) != cudaSuccess) return PSPEC_ERR_CUDA;
   record_launches(1);
   return PSPEC_OK;

@@ -1,117 +1,121 @@
 // append_kv.cu -- keys and values into the paged cache, rotated to their positions (one
 // launch), with the query rows rotated beside them.
 //
-// A CTA takes `rows_per_cta` rows.  Its threads first form the rows' angles pos * inv_freq in
-// fp64 (positions reach 10^6: an fp32 product would be off by 0.06 rad there) and their sine
-// and cosine, once for all heads; then every thread owns fixed elements of a head, keeps their
-// coefficients in registers and walks the heads.
+// A CTA takes `rows_per_cta` rows, all their heads in one list: every thread owns the same eight
+// elements of each head that it comes to, and fetches a few heads ahead, so that the CTA is
+// bound by what the memory delivers and not by one head's latency after another (a head at a
+// time: 179 us for 15360 rows of 80 heads of 64 bf16, 25 percent padding; so: TIMES).
+// Partners of the half split come from the lane that holds them where a head's lanes lie in one
+// warp.  The first heads are on their way while the sines and cosines of the rows' angles are
+// formed, once for all heads.  Angles pos * inv_freq are formed and reduced in fp64 (positions
+// reach 10^6: an fp32 product would be off by 0.06 rad there), rotations run in fp32.
 //
-// 4-bit cache: four lanes share a block of 16 elements (four each); the block's largest
-// magnitude goes round the four by shuffles.  Rotation and quantisation run in fp64: a value
-// next to the border of two codes takes the wrong one when it is off by anything, and the
-// borders mid * s * g (3 + 4 + 24 significant bits) are exact there, so no division is needed
-// per element and ties are seen as ties.
+// 4-bit cache: two lanes share a block of 16 elements.  Which code a value takes is decided as
+// if computed exactly, and fp32 decides nearly always: the scale and the codes are rounded at
+// both ends of the interval that holds the exact value, and where the ends differ (a few blocks
+// in ten thousand) the block is done again in fp64, whose borders mid * s * g (3 + 4 + 24
+// significant bits) are exact, so that ties are seen as ties.
 #include "common.cuh"
 #include "kernels.h"
+#include "plan.h"
 
 namespace pspec {
 
 namespace {
 
+constexpr int kMaxAppendRows = 4;        // of a CTA
+
 template <typename Tag> struct Row;
 template <> struct Row<BF16Tag> {
-  // 4 or 8 consecutive elements as floats; `vec`: the address is aligned to their size
-  static __device__ __forceinline__ void load4(const uint16_t* p, bool vec, float (&x)[4]) {
-    if (vec) {
-      const uint2 v = *reinterpret_cast<const uint2*>(p);
-      x[0] = bf16_lo(v.x); x[1] = bf16_hi(v.x); x[2] = bf16_lo(v.y); x[3] = bf16_hi(v.y);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) x[j] = __uint_as_float((uint32_t)p[j] << 16);
-    }
-  }
-  static __device__ __forceinline__ uint16_t round(float x) {
-    uint16_t r;
-    asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(r) : "f"(x));
-    return r;
-  }
+  static constexpr int kRaw = 1, kAhead = 4;    // 16-byte pieces of eight elements; heads in flight
   static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
   }
-  static __device__ __forceinline__ void store4(uint16_t* p, bool vec, const float (&x)[4]) {
+  static __device__ __forceinline__ void store8(uint16_t* p, bool vec, const float (&x)[8]) {
+    const uint4 v = make_uint4(pack(x[0], x[1]), pack(x[2], x[3]), pack(x[4], x[5]), pack(x[6], x[7]));
     if (vec) {
-      *reinterpret_cast<uint2*>(p) = make_uint2(pack(x[0], x[1]), pack(x[2], x[3]));
+      *reinterpret_cast<uint4*>(p) = v;
     } else {
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) p[j] = round(x[j]);
+      for (int j = 0; j < 8; ++j) p[j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
     }
   }
 };
 template <> struct Row<F32Tag> {
-  static __device__ __forceinline__ void load4(const float* p, bool vec, float (&x)[4]) {
+  static constexpr int kRaw = 2, kAhead = 2;
+  static __device__ __forceinline__ uint32_t pack(float lo, float) { return __float_as_uint(lo); }
+  static __device__ __forceinline__ void store8(float* p, bool vec, const float (&x)[8]) {
     if (vec) {
-      const float4 v = *reinterpret_cast<const float4*>(p);
-      x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+      reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+      reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
     } else {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) x[j] = p[j];
-    }
-  }
-  static __device__ __forceinline__ void store4(float* p, bool vec, const float (&x)[4]) {
-    if (vec) {
-      *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) p[j] = x[j];
+      for (int j = 0; j < 8; ++j) p[j] = x[j];
     }
   }
 };
 
-// The four consecutive elements j0 .. j0+3 that a thread owns in every head of one row: their
-// coefficients, and where their partners are.
-struct Turn {
-  double c[4], s[4];   // out_j = x_j c + partner_j s (s carries the sign)
-  int partner;         // offset of the partner of element 0; -1: inside the vector (x[j ^ 1])
-  unsigned mask;       // bit j: element j0 + j is rotated
-};
-
-__device__ __forceinline__ Turn make_turn(const double2* cs, int j0, int rot, bool interleaved) {
-  Turn t;
-  const int h = rot >> 1;
-  t.mask = 0;
-  t.partner = -1;
+// Eight consecutive elements as stored; `vec`: the address is aligned to 16 bytes.
+template <typename Tag>
+__device__ __forceinline__ void fetch8(const typename Tag::elem* p, bool vec, uint4 (&raw)[Row<Tag>::kRaw]) {
+  if (vec) {
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const int j = j0 + e;
-    t.c[e] = 1.0;
-    t.s[e] = 0.0;
-    if (j < rot) {
-      const double2 v = cs[interleaved ? j >> 1 : (j < h ? j : j - h)];
-      const bool first = interleaved ? !(j & 1) : j < h;
-      t.c[e] = v.x;
-      t.s[e] = first ? -v.y : v.y;
-      t.mask |= 1u << e;
+    for (int i = 0; i < Row<Tag>::kRaw; ++i) raw[i] = ld_stream(p + i * Tag::kVec);
+  } else {
+    constexpr int E = Tag::kVec / 4;                  // elements of a word
+#pragma unroll
+    for (int i = 0; i < Row<Tag>::kRaw; ++i) {
+      uint32_t w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int at = i * Tag::kVec + j * E;
+        w[j] = Row<Tag>::pack(load_scalar(p, at), E == 2 ? load_scalar(p, at + 1) : 0.f);
+      }
+      raw[i] = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
-  return t;
+}
+template <typename Tag>
+__device__ __forceinline__ void values8(const uint4 (&raw)[Row<Tag>::kRaw], float (&x)[8]) {
+#pragma unroll
+  for (int i = 0; i < Row<Tag>::kRaw; ++i) {
+    float y[Tag::kVec];
+    unpack(raw[i], y, Tag{});
+#pragma unroll
+    for (int j = 0; j < Tag::kVec; ++j) x[i * Tag::kVec + j] = y[j];
+  }
 }
 
-// The partners of elements j0 .. j0+3 of a head (half split): j + h below h, j - h from h on.
-template <typename Tag>
-__device__ __forceinline__ void load_partners(const typename Tag::elem* head, int j0, int rot,
-                                              bool vec, float (&p)[4]) {
-  const int h = rot >> 1;
-  if ((h & 3) == 0) {
-    Row<Tag>::load4(head + (j0 < h ? j0 + h : j0 - h), vec, p);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int j = j0 + e;
-      p[e] = j < rot ? load_scalar(head, j < h ? j + h : j - h) : 0.f;
-    }
-  }
+// Sine and cosine of the fp64 angle a, |a| < 2^31: reduced to |r| <= pi/4 by multiples of pi/2
+// (two terms of it), then the Taylor polynomials (remainders below 5e-17).
+__device__ __forceinline__ void turn_of(double a, double& sine, double& cosine) {
+  const double n = rint(a * 0.63661977236758134308);
+  double r = fma(-n, 1.57079632679489661923, a);
+  r = fma(-n, 6.12323399573676603587e-17, r);
+  const double q = r * r;
+  double s = fma(q, -1.0 / 1307674368000.0, 1.0 / 6227020800.0);
+  s = fma(q, s, -1.0 / 39916800.0);
+  s = fma(q, s, 1.0 / 362880.0);
+  s = fma(q, s, -1.0 / 5040.0);
+  s = fma(q, s, 1.0 / 120.0);
+  s = fma(q, s, -1.0 / 6.0);
+  s = fma(q * r, s, r);
+  double c = fma(q, 1.0 / 20922789888000.0, -1.0 / 87178291200.0);
+  c = fma(q, c, 1.0 / 479001600.0);
+  c = fma(q, c, -1.0 / 3628800.0);
+  c = fma(q, c, 1.0 / 40320.0);
+  c = fma(q, c, -1.0 / 720.0);
+  c = fma(q, c, 1.0 / 24.0);
+  c = fma(q, c, -0.5);
+  c = fma(q, c, 1.0);
+  const int k = (int)((long long)n & 3);
+  sine = k & 1 ? c : s;
+  cosine = k & 1 ? s : c;
+  if (k & 2) sine = -sine;
+  if ((k + 1) & 2) cosine = -cosine;
 }
 
 // A block scale: the e4m3 value nearest to a >= 0 (ties to even, at most 448) and its code.
@@ -150,151 +154,305 @@ __device__ __forceinline__ float e2m1_value(unsigned code) {
   return code & 8u ? -v : v;
 }
 
-template <typename Tag, bool kE2M1>
-__global__ void __launch_bounds__(kThreads) append_kernel(const AppendLaunch L) {
+// Two values to a byte of codes (lo in the low nibble), two to e4m3 bytes; rounded to nearest
+// even, at most the largest.
+__device__ __forceinline__ uint32_t codes_of(float lo, float hi) {
+  uint32_t d;
+  asm("{\n\t.reg .b8 b;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %2, %1;\n\tcvt.u32.u8 %0, b;\n\t}" : "=r"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ uint32_t scales_of(float lo, float hi) {
+  uint16_t d;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;" : "=h"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ float e4m3_value(unsigned code) {  // finite, not negative
+  const unsigned e = code >> 3, m = code & 7u;
+  return e ? __uint_as_float((e + 120u) << 23 | m << 20) : (float)m * 0.001953125f;
+}
+
+// A block's half (elements j0 .. j0+7 of `head`) in fp64, both lanes of the block: eight codes,
+// the scale's code in `sc`.  pos < 0 and j < rot together: no rotation.
+template <typename Tag>
+__device__ __noinline__ uint32_t exact_codes(const typename Tag::elem* head, int j0, int rot, bool interleaved,
+                                             int pos, const float* inv_freq, float g, unsigned& sc) {
+  const int h = rot >> 1;
+  double x[8], top = 0.0;
+  for (int e = 0; e < 8; ++e) {
+    const int j = j0 + e;
+    x[e] = (double)load_scalar(head, j);
+    if (j < rot) {
+      const bool first = interleaved ? !(j & 1) : j < h;
+      const double p = (double)load_scalar(head, interleaved ? j ^ 1 : (first ? j + h : j - h));
+      double s, c;
+      turn_of((double)pos * (double)__ldg(inv_freq + (interleaved ? j >> 1 : (first ? j : j - h))), s, c);
+      x[e] = fma(x[e], c, first ? -(p * s) : p * s);
+    }
+    top = fmax(top, fabs(x[e]));                              // drops NaN
+  }
+  top = fmax(top, __shfl_xor_sync(3u << (threadIdx.x & 30), top, 1));
+  const double s = e4m3_round(top / (double)g / 6.0, sc), u = s * (double)g;
+  uint32_t packed = 0;
+  for (int e = 0; e < 8; ++e) {
+    unsigned code = s > 0.0 ? e2m1_code(fabs(x[e]), u) : 0u;
+    code |= x[e] == x[e] && signbit(x[e]) ? 8u : 0u;
+    packed |= code << (4 * e);
+  }
+  return packed;
+}
+
+// How partners are found.
+enum { kAnyhow, kByLane, kInterleaved };   // the first for any rows; the others for 16-byte aligned
+
+template <typename Tag, bool kE2M1, int kMode>
+__global__ void __launch_bounds__(kThreads, 3) append_kernel(const AppendLaunch L) {
   using elem = typename Tag::elem;
-  extern __shared__ double2 s_cs[];                   // [rows_per_cta][rot / 2] (cos, sin)
+  constexpr int kRaw = Row<Tag>::kRaw, kAhead = kMode == kAnyhow ? 1 : Row<Tag>::kAhead;
+  extern __shared__ __align__(16) float2 s_cs[];      // [rows_per_cta][rot / 2] (cos, sin)
+  __shared__ long long s_row[kMaxAppendRows];         // the row's place under head 0; -1: none
   const pspec_append_args& a = L.a;
   const int tid = threadIdx.x;
   const int h = a.rot >> 1;
   const long long t0 = (long long)blockIdx.x * L.rows_per_cta;
   const int rows = (int)min((long long)L.rows_per_cta, a.T - t0);
 
-  for (int i = tid; i < rows * h; i += kThreads) {
-    const int r = i / h, j = i - r * h;
-    if (__ldg(a.slot_mapping + t0 + r) < 0) continue;
-    double s, c;
-    sincos((double)__ldg(a.positions + t0 + r) * (double)__ldg(a.inv_freq + j), &s, &c);
-    s_cs[i] = make_double2(c, s);
+  if (tid < rows) {
+    const long long slot = __ldg(reinterpret_cast<const long long*>(a.slot_mapping) + t0 + tid);
+    long long at = -1;
+    if (slot >= 0 && slot < L.slots) {
+      const long long block = L.slots <= 0x7fffffff ? (unsigned)slot / (unsigned)a.block_size : slot / a.block_size;
+      at = block * a.Hkv * a.block_size + (slot - block * a.block_size);
+    } else if (slot != PSPEC_PADDING_SLOT_ID) {
+      set_err(a.err, PSPEC_DEVERR_BLOCK_RANGE);
+    }
+    s_row[tid] = at;
   }
   __syncthreads();
 
-  const int nl = a.D >> 2;                            // threads per head, four elements each
+  const int nl = a.D >> 3;                            // threads per head, eight elements each
   const int groups = kThreads / nl;
-  const int hg = tid / nl, j0 = (tid - hg * nl) * 4;
-  const bool mine = hg < groups;
-  const unsigned quad = 0xfu << (tid & 28);
-  for (int r = 0; r < rows; ++r) {
-    const long long t = t0 + r;
-    const long long slot = __ldg(reinterpret_cast<const long long*>(a.slot_mapping) + t);
-    if (slot < 0 || slot >= L.slots) {
-      if (tid == 0 && slot != PSPEC_PADDING_SLOT_ID) set_err(a.err, PSPEC_DEVERR_BLOCK_RANGE);
-      continue;
+  const int hg = tid / nl, j0 = (tid - hg * nl) * 8;
+  const bool turns = j0 < a.rot;
+  const bool low = j0 < h;                            // (half split) partners lie above
+  const int from = (low ? tid + (h >> 3) : tid - (h >> 3)) & 31;
+
+  // The heads of one kind, rows x heads of them in a list: each thread's in batches of kAhead.
+  struct List {
+    const elem* src;         // of the CTA's first row
+    long long stride;
+    int heads;
+    bool vec;
+    int total;               // 0: none
+  };
+  auto locate = [&](const List& l, int i, int& r, int& hd) {   // false: nothing to do there
+    r = (int)((unsigned)min(i, l.total - 1) / (unsigned)l.heads);
+    hd = min(i, l.total - 1) - r * l.heads;
+    return hg < groups && i < l.total && s_row[r] >= 0;
+  };
+  auto fetch = [&](const List& l, int i0, uint4 (&raw)[kAhead][kRaw]) {
+#pragma unroll
+    for (int b = 0; b < kAhead; ++b) {
+#pragma unroll
+      for (int i = 0; i < kRaw; ++i) raw[b][i] = make_uint4(0, 0, 0, 0);
+      int r, hd;
+      if (i0 + b * groups < l.total && locate(l, hg + i0 + b * groups, r, hd))
+        fetch8<Tag>(l.src + r * l.stride + (long long)hd * a.D + j0, kMode != kAnyhow || l.vec, raw[b]);
     }
-    if (!mine) continue;
-    const long long block = slot / a.block_size;
-    const int off = (int)(slot - block * a.block_size);
-    const Turn turn = make_turn(s_cs + r * h, j0, a.rot, a.interleaved != 0);
-
-    // rotated in fp32: the result is rounded to the rows' dtype, no border to decide
-    auto turned = [&](const elem* head, bool vec, float (&x)[4]) {
-      Row<Tag>::load4(head + j0, vec, x);
-      if (!turn.mask) return;
-      float p[4];
-      if (a.interleaved) {
+  };
+  // x turned, of a head at src in row r; the largest magnitudes that entered, added.  Every lane
+  // of the warp comes here.
+  auto turn = [&](const elem* src, int r, bool ok, const uint4 (&raw)[kRaw], float (&x)[8]) {
+    float p[8], reach = 0.f, most = 0.f;
+    if constexpr (kMode == kByLane) {
+      // (the sign of the sine with the partners')
+      const uint32_t flip = !low ? 0u : (sizeof(elem) == 2 ? 0x80008000u : 0x80000000u);
+      uint4 o[kRaw];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) p[e] = x[e ^ 1];
-      } else {
-        load_partners<Tag>(head, j0, a.rot, vec, p);
+      for (int i = 0; i < kRaw; ++i)
+        o[i] = make_uint4(__shfl_sync(0xffffffffu, raw[i].x, from) ^ flip, __shfl_sync(0xffffffffu, raw[i].y, from) ^ flip,
+                          __shfl_sync(0xffffffffu, raw[i].z, from) ^ flip, __shfl_sync(0xffffffffu, raw[i].w, from) ^ flip);
+      values8<Tag>(o, p);
+    }
+    if (!turns || !ok) return 0.f;
+    if constexpr (kMode == kByLane) {                 // whole threads turn
+      const float4* cs = reinterpret_cast<const float4*>(s_cs + r * h + (low ? j0 : j0 - h));
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) {
+        const float4 v = cs[e >> 1];
+        reach = fmaxf(reach, fmaxf(fabsf(x[e]), fabsf(x[e + 1])));
+        most = fmaxf(most, fmaxf(fabsf(p[e]), fabsf(p[e + 1])));
+        x[e] = fmaf(x[e], v.x, p[e] * v.y);
+        x[e + 1] = fmaf(x[e + 1], v.z, p[e + 1] * v.w);
       }
+    } else if (kMode == kInterleaved || a.interleaved) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (turn.mask >> e & 1) x[e] = fmaf(x[e], (float)turn.c[e], p[e] * (float)turn.s[e]);
-    };
-
-    if (a.q) {
-      const elem* q = static_cast<const elem*>(a.q) + t * a.q_stride;
-      elem* o = static_cast<elem*>(a.q_out) + t * (long long)a.Hq * a.D;
-      for (int hd = hg; hd < a.Hq; hd += groups) {
-        float x[4];
-        turned(q + (long long)hd * a.D, L.vec_q, x);
-        Row<Tag>::store4(o + (long long)hd * a.D + j0, L.vec_qo, x);
+      for (int e = 0; e < 8; e += 2) {
+        if (j0 + e < a.rot) {
+          const float2 v = s_cs[r * h + ((j0 + e) >> 1)];
+          const float u = x[e], w = x[e + 1];
+          reach = fmaxf(reach, fmaxf(fabsf(u), fabsf(w)));
+          x[e] = fmaf(u, v.x, -(w * v.y));
+          x[e + 1] = fmaf(w, v.x, u * v.y);
+        }
+      }
+      most = reach;
+    } else {
+#pragma unroll 1
+      for (int j = j0; j < min(j0 + 8, a.rot); ++j) {
+        const bool under = j < h;
+        const float2 v = s_cs[r * h + (under ? j : j - h)];
+        const float u = load_scalar(src, j), w = load_scalar(src, under ? j + h : j - h);
+        reach = fmaxf(reach, fabsf(u));
+        most = fmaxf(most, fabsf(w));
+        const float y = fmaf(u, v.x, w * (under ? -v.y : v.y));
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = j0 + e == j ? y : x[e];
       }
     }
+    return reach + most;
+  };
 
-    const elem* kr = static_cast<const elem*>(a.k) + t * a.k_stride;
-    const elem* vr = static_cast<const elem*>(a.v) + t * a.v_stride;
-    for (int i = hg; i < 2 * a.Hkv; i += groups) {    // the key heads, then the value heads
-      const bool is_k = i < a.Hkv;
-      const int hd = is_k ? i : i - a.Hkv;
-      const elem* head = (is_k ? kr : vr) + (long long)hd * a.D;
-      const bool vec = is_k ? L.vec_k : L.vec_v;
-      const long long row = (block * a.Hkv + hd) * a.block_size + off;   // row of the cache
-      elem* echo = static_cast<elem*>(is_k ? a.k_out : a.v_out);
-      if (echo) echo += (t * a.Hkv + hd) * a.D + j0;
-      const bool vec_e = is_k ? L.vec_ko : L.vec_vo;
-      if constexpr (!kE2M1) {
-        float x[4];
-        if (is_k) turned(head, vec, x);
-        else Row<Tag>::load4(head + j0, vec, x);
-        elem* dst = static_cast<elem*>(is_k ? a.k_pages : a.v_pages) + row * a.D + j0;
-        Row<Tag>::store4(dst, true, x);
-        if (echo) Row<Tag>::store4(echo, vec_e, x);
-      } else {
-        float xf[4];
-        Row<Tag>::load4(head + j0, vec, xf);
-        double x[4];
+  const List ql = {static_cast<const elem*>(a.q) + t0 * a.q_stride, a.q_stride, a.Hq, L.vec_q, a.q ? rows * a.Hq : 0};
+  uint4 raw[kAhead][kRaw];
+  fetch(ql, 0, raw);
+
+  for (int i = tid; i < rows * h; i += kThreads) {
+    const int r = i / h, j = i - r * h;
+    if (s_row[r] < 0) continue;
+    double s, c;
+    turn_of((double)__ldg(a.positions + t0 + r) * (double)__ldg(a.inv_freq + j), s, c);
+    s_cs[i] = make_float2((float)c, (float)s);
+  }
+  __syncthreads();
+
+  for (int i0 = 0; i0 < ql.total; i0 += kAhead * groups) {    // the same for every thread
+    if (i0 > 0) fetch(ql, i0, raw);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = xf[e];
-        if (is_k && turn.mask) {
-          float p[4];
-          if (a.interleaved) {
+    for (int b = 0; b < kAhead; ++b) {
+      if (i0 + b * groups >= ql.total) break;
+      int r, hd;
+      const bool ok = locate(ql, hg + i0 + b * groups, r, hd);
+      float x[8];
+      values8<Tag>(raw[b], x);
+      turn(ql.src + r * ql.stride + (long long)hd * a.D, r, ok, raw[b], x);
+      if (ok)
+        Row<Tag>::store8(static_cast<elem*>(a.q_out) + ((t0 + r) * a.Hq + hd) * a.D + j0, kMode != kAnyhow || L.vec_qo, x);
+    }
+  }
+
+#pragma unroll 1
+  for (int kind = 0; kind < 2; ++kind) {
+    const bool is_k = kind == 0;
+    const long long stride = is_k ? a.k_stride : a.v_stride;
+    const List l = {static_cast<const elem*>(is_k ? a.k : a.v) + t0 * stride, stride, a.Hkv, is_k ? L.vec_k : L.vec_v,
+                    rows * a.Hkv};
+    elem* echo_all = static_cast<elem*>(is_k ? a.k_out : a.v_out);
+    const bool vec_e = kMode != kAnyhow || (is_k ? L.vec_ko : L.vec_vo);
+    for (int i0 = 0; i0 < l.total; i0 += kAhead * groups) {
+      fetch(l, i0, raw);
+#pragma unroll 1
+      for (int b = 0; b < kAhead; ++b) {
+        if (i0 + b * groups >= l.total) break;
+        int r, hd;
+        const bool ok = locate(l, hg + i0 + b * groups, r, hd);
+        const elem* src = l.src + r * l.stride + (long long)hd * a.D;
+        float x[8], reach = 0.f;
+        values8<Tag>(raw[0], x);
+        if (is_k) reach = turn(src, r, ok, raw[0], x);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) p[e] = xf[e ^ 1];
-          } else {
-            load_partners<Tag>(head, j0, a.rot, vec, p);
+        for (int c = 0; c + 1 < kAhead; ++c)              // the next one to the front
+#pragma unroll
+          for (int i = 0; i < kRaw; ++i) raw[c][i] = raw[c + 1][i];
+        if (!ok) continue;
+        const long long t = t0 + r;
+        const long long row = s_row[r] + (long long)hd * a.block_size;   // row of the cache
+        elem* echo = echo_all ? echo_all + (t * a.Hkv + hd) * a.D + j0 : nullptr;
+        if constexpr (!kE2M1) {
+          Row<Tag>::store8(static_cast<elem*>(is_k ? a.k_pages : a.v_pages) + row * a.D + j0, true, x);
+          if (echo) Row<Tag>::store8(echo, vec_e, x);
+        } else {
+          const unsigned pair = 3u << (tid & 30);
+          // |fp32 value - exact value| <= err: the coefficients are off by 2^-24, products and sum
+          // rounded, 2.5 * 2^-24 of the two magnitudes; 2^-20 leaves room
+          float err = reach * 9.5367432e-7f, top = 0.f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[e]));   // drops NaN
+          top = fmaxf(top, __shfl_xor_sync(pair, top, 1));
+          const float err2 = fmaxf(err, __shfl_xor_sync(pair, err, 1));
+          const float* scales = is_k ? a.k_scale : a.v_scale;
+          const float g = scales ? __ldg(scales + hd) : 1.f;
+          // the scale from both ends of its interval (the quotients are off by 2^-21 at most)
+          const float per6 = 1.f / (6.f * g), mid = top * per6;
+          const float wide = fmaf(mid, 1e-6f, err2 * per6);
+          const unsigned ends = scales_of(fmaxf(mid - wide, 0.f), mid + wide);
+          unsigned sc = ends & 0xffu;
+          const float s = e4m3_value(sc), per = s > 0.f ? 1.f / (s * g) : 0.f;
+          uint32_t packed = 0;
+          bool sure = ends == sc * 0x101u && wide <= 1e30f;
+          const float room = err * per;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const float z0 = x[2 * c] * per, z1 = x[2 * c + 1] * per;
+            const float w0 = fmaf(fabsf(z0), 1e-6f, room), w1 = fmaf(fabsf(z1), 1e-6f, room);
+            const uint32_t lo = codes_of(z0 - w0, z1 - w1), hi = codes_of(z0 + w0, z1 + w1);
+            // (NaN, and the sign of a zero that may be either side: not sure)
+            sure = sure && lo == hi && z0 == z0 && z1 == z1;
+            packed |= lo << (8 * c);
           }
+          sure = __shfl_xor_sync(pair, sure, 1) && sure;
+          if (!sure)
+            packed = exact_codes<Tag>(src, j0, is_k ? a.rot : 0, a.interleaved != 0, __ldg(a.positions + t), a.inv_freq, g, sc);
+          uint8_t* pages = static_cast<uint8_t*>(is_k ? a.k_pages : a.v_pages);
+          *reinterpret_cast<uint32_t*>(pages + row * (a.D >> 1) + (j0 >> 1)) = packed;
+          if ((j0 & 15) == 0) {
+            uint8_t* bs = static_cast<uint8_t*>(is_k ? a.k_block_scales : a.v_block_scales);
+            bs[row * (a.D >> 4) + (j0 >> 4)] = (uint8_t)sc;
+          }
+          if (echo) {                                 // level * s is exact, one rounding with g
+            const float sv = e4m3_value(sc);
+            float v[8];
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (turn.mask >> e & 1) x[e] = fma((double)xf[e], turn.c[e], (double)p[e] * turn.s[e]);
-        }
-        double top = 0.0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) top = fmax(top, fabs(x[e]));   // drops NaN
-        top = fmax(top, __shfl_xor_sync(quad, top, 1));
-        top = fmax(top, __shfl_xor_sync(quad, top, 2));
-        const float* scales = is_k ? a.k_scale : a.v_scale;
-        const float g = scales ? __ldg(scales + hd) : 1.f;
-        unsigned sc;
-        const double s = e4m3_round(top / (double)g / 6.0, sc);
-        const double u = s * (double)g;
-        unsigned code[4], packed = 0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          code[e] = s > 0.0 ? e2m1_code(fabs(x[e]), u) : 0u;
-          code[e] |= x[e] == x[e] && signbit(x[e]) ? 8u : 0u;
-          packed |= code[e] << (4 * e);
-        }
-        uint8_t* pages = static_cast<uint8_t*>(is_k ? a.k_pages : a.v_pages);
-        *reinterpret_cast<uint16_t*>(pages + row * (a.D >> 1) + (j0 >> 1)) = (uint16_t)packed;
-        if ((j0 & 15) == 0) {
-          uint8_t* bs = static_cast<uint8_t*>(is_k ? a.k_block_scales : a.v_block_scales);
-          bs[row * (a.D >> 4) + (j0 >> 4)] = (uint8_t)sc;
-        }
-        if (echo) {                                   // level * s is exact, one rounding with g
-          float v[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] = e2m1_value(code[e]) * (float)s * g;
-          Row<Tag>::store4(echo, vec_e, v);
+            for (int e = 0; e < 8; ++e) v[e] = e2m1_value(packed >> (4 * e)) * sv * g;
+            Row<Tag>::store8(echo, vec_e, v);
+          }
         }
       }
     }
   }
 }
 
+template <typename Tag>
+void launch_rows(const AppendLaunch& L, cudaStream_t stream) {
+  const pspec_append_args& a = L.a;
+  const unsigned grid = (unsigned)((a.T + L.rows_per_cta - 1) / L.rows_per_cta);
+  const size_t smem = (size_t)L.rows_per_cta * (a.rot / 2) * sizeof(float2);
+  const bool aligned = (!a.q || (L.vec_q && L.vec_qo)) && L.vec_k && L.vec_v && L.vec_ko && L.vec_vo;
+  // partners in another lane: a head's lanes lie in one warp, whole threads on each side
+  const int nl = a.D / 8;
+  int mode = kAnyhow;
+  if (aligned && a.rot == 0) mode = kInterleaved;
+  else if (aligned && a.interleaved) mode = kInterleaved;
+  else if (aligned && (nl & (nl - 1)) == 0 && nl <= 32 && a.rot % 16 == 0) mode = kByLane;
+  auto go = [&](auto* fn) { fn<<<grid, kThreads, smem, stream>>>(L); };
+  if (a.cache == PSPEC_CACHE_E2M1) {
+    if (mode == kByLane) go(append_kernel<Tag, true, kByLane>);
+    else if (mode == kInterleaved) go(append_kernel<Tag, true, kInterleaved>);
+    else go(append_kernel<Tag, true, kAnyhow>);
+  } else {
+    if (mode == kByLane) go(append_kernel<Tag, false, kByLane>);
+    else if (mode == kInterleaved) go(append_kernel<Tag, false, kInterleaved>);
+    else go(append_kernel<Tag, false, kAnyhow>);
+  }
+}
+
 }  // namespace
 
-cudaError_t launch_append(const AppendLaunch& L, cudaStream_t stream) {
-  const unsigned grid = (unsigned)((L.a.T + L.rows_per_cta - 1) / L.rows_per_cta);
-  const size_t smem = (size_t)L.rows_per_cta * (L.a.rot / 2) * sizeof(double2);
-  const bool e2m1 = L.a.cache == PSPEC_CACHE_E2M1;
-  if (L.a.dtype == PSPEC_BF16) {
-    if (e2m1) append_kernel<BF16Tag, true><<<grid, kThreads, smem, stream>>>(L);
-    else append_kernel<BF16Tag, false><<<grid, kThreads, smem, stream>>>(L);
-  } else {
-    if (e2m1) append_kernel<F32Tag, true><<<grid, kThreads, smem, stream>>>(L);
-    else append_kernel<F32Tag, false><<<grid, kThreads, smem, stream>>>(L);
-  }
+cudaError_t launch_append(const AppendLaunch& in, cudaStream_t stream) {
+  AppendLaunch L = in;
+  // a row to a CTA while there are few
+  L.rows_per_cta = L.a.T <= 2 * kNumSMs ? 1 : (L.a.T <= 16 * kNumSMs ? 2 : kMaxAppendRows);
+  if (L.a.dtype == PSPEC_BF16) launch_rows<BF16Tag>(L, stream);
+  else launch_rows<F32Tag>(L, stream);
   return cudaGetLastError();
 }
 

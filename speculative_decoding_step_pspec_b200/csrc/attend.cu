@@ -755,14 +755,19 @@ cudaError_t launch_nt(AttendLaunch L, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
-// Tiles for the rows that a sequence has on average.
+// The largest tiles that still give every CTA one: fewer leave each to many CTAs, whose results
+// take longer to join than a code takes to be converted again (8 rows of 64 heads over 4096 keys:
+// TIMES).
 template <int D, typename Tag>
 cudaError_t launch_d(const AttendLaunch& L, cudaStream_t stream) {
   const long long rows = ((long long)L.a.T * (L.a.Hq / L.a.Hkv) + L.a.B - 1) / L.a.B;
   constexpr int most = D == 64 && sizeof(typename Tag::elem) == 2 ? 4 : 2;
-  if (rows <= 8) return launch_nt<D, Tag, 1>(L, stream);
-  if (rows <= 16 || most == 2) return launch_nt<D, Tag, 2>(L, stream);
-  return launch_nt<D, Tag, most>(L, stream);
+  const auto fits = [&](int nt) {
+    return rows > 4 * nt && (long long)L.a.B * L.a.Hkv * ((rows + 8 * nt - 1) / (8 * nt)) >= 3 * kNumSMs;
+  };
+  if (most == 4 && fits(4)) return launch_nt<D, Tag, most>(L, stream);
+  if (fits(2)) return launch_nt<D, Tag, 2>(L, stream);
+  return launch_nt<D, Tag, 1>(L, stream);
 }
 
 }  // namespace

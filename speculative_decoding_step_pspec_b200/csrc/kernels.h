@@ -132,7 +132,7 @@ struct AppendLaunch {
   pspec_append_args a;
   int rows_per_cta;
   long long slots;                // num_blocks * block_size
-  bool vec_q, vec_k, vec_v;       // rows whose four-element groups are aligned to their size
+  bool vec_q, vec_k, vec_v;       // rows whose eight-element groups are 16-byte aligned
   bool vec_qo, vec_ko, vec_vo;
 };
 cudaError_t launch_append(const AppendLaunch& L, cudaStream_t stream);
