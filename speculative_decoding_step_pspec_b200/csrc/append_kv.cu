@@ -236,32 +236,50 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(const AppendLaunch 
   const bool low = j0 < h;                            // (half split) partners lie above
   const int from = (low ? tid + (h >> 3) : tid - (h >> 3)) & 31;
 
-  // The heads of one kind, rows x heads of them in a list: each thread's in batches of kAhead.
-  struct List {
-    const elem* src;         // of the CTA's first row
-    long long stride;
-    int heads;
-    bool vec;
-    int total;               // 0: none
+  // Query heads, and key then value heads, rows x heads of them in a list: each thread has every
+  // groups-th from its hg-th on.
+  struct Cursor {
+    int r, hd, heads, step_r, step_h;
+    __device__ __forceinline__ Cursor(int at, int n, int step)
+        : r(at / n), hd(at % n), heads(n), step_r(step / n), step_h(step % n) {}
+    __device__ __forceinline__ void next() {
+      r += step_r;
+      hd += step_h;
+      if (hd >= heads) {
+        hd -= heads;
+        ++r;
+      }
+    }
   };
-  auto locate = [&](const List& l, int i, int& r, int& hd) {   // false: nothing to do there
-    r = (int)((unsigned)min(i, l.total - 1) / (unsigned)l.heads);
-    hd = min(i, l.total - 1) - r * l.heads;
-    return hg < groups && i < l.total && s_row[r] >= 0;
+  auto there = [&](const Cursor& c) { return hg < groups && c.r < rows && s_row[c.r] >= 0; };
+  const int total_q = a.q ? rows * a.Hq : 0, total_kv = rows * 2 * a.Hkv;
+  Cursor at_q(hg, max(1, a.Hq), groups), at_kv(hg, 2 * a.Hkv, groups), ahead_q = at_q, ahead_kv = at_kv;
+  auto src_q = [&](int r, int hd) {
+    return static_cast<const elem*>(a.q) + (t0 + r) * a.q_stride + (long long)hd * a.D;
   };
-  auto fetch = [&](const List& l, int i0, uint4 (&raw)[kAhead][kRaw]) {
+  auto src_kv = [&](int r, int hd) {
+    return hd < a.Hkv ? static_cast<const elem*>(a.k) + (t0 + r) * a.k_stride + (long long)hd * a.D
+                      : static_cast<const elem*>(a.v) + (t0 + r) * a.v_stride + (long long)(hd - a.Hkv) * a.D;
+  };
+  auto fetch_q = [&](int i0, uint4 (&raw)[kAhead][kRaw]) {
 #pragma unroll
     for (int b = 0; b < kAhead; ++b) {
-#pragma unroll
-      for (int i = 0; i < kRaw; ++i) raw[b][i] = make_uint4(0, 0, 0, 0);
-      int r, hd;
-      if (i0 + b * groups < l.total && locate(l, hg + i0 + b * groups, r, hd))
-        fetch8<Tag>(l.src + r * l.stride + (long long)hd * a.D + j0, kMode != kAnyhow || l.vec, raw[b]);
+      if (i0 + b * groups < total_q) {
+        if (there(ahead_q)) fetch8<Tag>(src_q(ahead_q.r, ahead_q.hd) + j0, kMode != kAnyhow || L.vec_q, raw[b]);
+        ahead_q.next();
+      }
+    }
+  };
+  auto fetch_kv = [&](int i0, uint4 (&raw)[kRaw]) {
+    if (i0 < total_kv) {
+      const Cursor& c = ahead_kv;
+      if (there(c)) fetch8<Tag>(src_kv(c.r, c.hd) + j0, kMode != kAnyhow || (c.hd < a.Hkv ? L.vec_k : L.vec_v), raw);
+      ahead_kv.next();
     }
   };
   // x turned, of a head at src in row r; the largest magnitudes that entered, added.  Every lane
   // of the warp comes here.
-  auto turn = [&](const elem* src, int r, bool ok, const uint4 (&raw)[kRaw], float (&x)[8]) {
+  auto turn = [&](const elem* src, int r, bool ok, bool wanted, const uint4 (&raw)[kRaw], float (&x)[8]) {
     float p[8], reach = 0.f, most = 0.f;
     if constexpr (kMode == kByLane) {
       // (the sign of the sine with the partners')
@@ -273,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(const AppendLaunch 
                           __shfl_sync(0xffffffffu, raw[i].z, from) ^ flip, __shfl_sync(0xffffffffu, raw[i].w, from) ^ flip);
       values8<Tag>(o, p);
     }
-    if (!turns || !ok) return 0.f;
+    if (!turns || !ok || !wanted) return 0.f;
     if constexpr (kMode == kByLane) {                 // whole threads turn
       const float4* cs = reinterpret_cast<const float4*>(s_cs + r * h + (low ? j0 : j0 - h));
 #pragma unroll
@@ -312,9 +330,10 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(const AppendLaunch 
     return reach + most;
   };
 
-  const List ql = {static_cast<const elem*>(a.q) + t0 * a.q_stride, a.q_stride, a.Hq, L.vec_q, a.q ? rows * a.Hq : 0};
-  uint4 raw[kAhead][kRaw];
-  fetch(ql, 0, raw);
+  uint4 raw[kAhead][kRaw] = {}, next[2][kRaw] = {};   // key and value heads two ahead
+  fetch_kv(0, next[0]);
+  fetch_kv(groups, next[1]);
+  fetch_q(0, raw);
 
   for (int i = tid; i < rows * h; i += kThreads) {
     const int r = i / h, j = i - r * h;
@@ -325,97 +344,87 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(const AppendLaunch 
   }
   __syncthreads();
 
-  for (int i0 = 0; i0 < ql.total; i0 += kAhead * groups) {    // the same for every thread
-    if (i0 > 0) fetch(ql, i0, raw);
+  for (int i0 = 0; i0 < total_q; i0 += kAhead * groups) {     // the same for every thread
+    if (i0 > 0) fetch_q(i0, raw);
 #pragma unroll
     for (int b = 0; b < kAhead; ++b) {
-      if (i0 + b * groups >= ql.total) break;
-      int r, hd;
-      const bool ok = locate(ql, hg + i0 + b * groups, r, hd);
+      if (i0 + b * groups >= total_q) break;
+      const bool ok = there(at_q);
+      const int r = min(at_q.r, rows - 1), hd = at_q.hd;
+      at_q.next();
       float x[8];
       values8<Tag>(raw[b], x);
-      turn(ql.src + r * ql.stride + (long long)hd * a.D, r, ok, raw[b], x);
+      turn(src_q(r, hd), r, ok, true, raw[b], x);
       if (ok)
         Row<Tag>::store8(static_cast<elem*>(a.q_out) + ((t0 + r) * a.Hq + hd) * a.D + j0, kMode != kAnyhow || L.vec_qo, x);
     }
   }
 
 #pragma unroll 1
-  for (int kind = 0; kind < 2; ++kind) {
-    const bool is_k = kind == 0;
-    const long long stride = is_k ? a.k_stride : a.v_stride;
-    const List l = {static_cast<const elem*>(is_k ? a.k : a.v) + t0 * stride, stride, a.Hkv, is_k ? L.vec_k : L.vec_v,
-                    rows * a.Hkv};
+  for (int i0 = 0; i0 < total_kv; i0 += groups) {
+    const bool ok = there(at_kv), is_k = at_kv.hd < a.Hkv;
+    const int r = min(at_kv.r, rows - 1), hd = is_k ? at_kv.hd : at_kv.hd - a.Hkv;
+    const elem* src = src_kv(r, at_kv.hd);
+    at_kv.next();
+    float x[8];
+    values8<Tag>(next[0], x);
+    const float reach = turn(src, r, ok, is_k, next[0], x);
+#pragma unroll
+    for (int i = 0; i < kRaw; ++i) next[0][i] = next[1][i];
+    fetch_kv(i0 + 2 * groups, next[1]);
+    if (!ok) continue;
     elem* echo_all = static_cast<elem*>(is_k ? a.k_out : a.v_out);
     const bool vec_e = kMode != kAnyhow || (is_k ? L.vec_ko : L.vec_vo);
-    for (int i0 = 0; i0 < l.total; i0 += kAhead * groups) {
-      fetch(l, i0, raw);
-#pragma unroll 1
-      for (int b = 0; b < kAhead; ++b) {
-        if (i0 + b * groups >= l.total) break;
-        int r, hd;
-        const bool ok = locate(l, hg + i0 + b * groups, r, hd);
-        const elem* src = l.src + r * l.stride + (long long)hd * a.D;
-        float x[8], reach = 0.f;
-        values8<Tag>(raw[0], x);
-        if (is_k) reach = turn(src, r, ok, raw[0], x);
+    const long long t = t0 + r;
+    const long long row = s_row[r] + (long long)hd * a.block_size;   // row of the cache
+    elem* echo = echo_all ? echo_all + (t * a.Hkv + hd) * a.D + j0 : nullptr;
+    if constexpr (!kE2M1) {
+      Row<Tag>::store8(static_cast<elem*>(is_k ? a.k_pages : a.v_pages) + row * a.D + j0, true, x);
+      if (echo) Row<Tag>::store8(echo, vec_e, x);
+    } else {
+      const unsigned pair = 3u << (tid & 30);
+      // |fp32 value - exact value| <= err: the coefficients are off by 2^-24, products and sum
+      // rounded, 2.5 * 2^-24 of the two magnitudes; 2^-20 leaves room
+      float err = reach * 9.5367432e-7f, top = 0.f;
 #pragma unroll
-        for (int c = 0; c + 1 < kAhead; ++c)              // the next one to the front
+      for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[e]));   // drops NaN
+      top = fmaxf(top, __shfl_xor_sync(pair, top, 1));
+      const float err2 = fmaxf(err, __shfl_xor_sync(pair, err, 1));
+      const float* scales = is_k ? a.k_scale : a.v_scale;
+      const float g = scales ? __ldg(scales + hd) : 1.f;
+      // the scale from both ends of its interval (the quotients are off by 2^-21 at most)
+      const float per6 = 1.f / (6.f * g), mid = top * per6;
+      const float wide = fmaf(mid, 1e-6f, err2 * per6);
+      const unsigned ends = scales_of(fmaxf(mid - wide, 0.f), mid + wide);
+      unsigned sc = ends & 0xffu;
+      const float s = e4m3_value(sc), per = s > 0.f ? 1.f / (s * g) : 0.f;
+      uint32_t packed = 0;
+      bool sure = ends == sc * 0x101u && wide <= 1e30f;
+      const float room = err * per;
 #pragma unroll
-          for (int i = 0; i < kRaw; ++i) raw[c][i] = raw[c + 1][i];
-        if (!ok) continue;
-        const long long t = t0 + r;
-        const long long row = s_row[r] + (long long)hd * a.block_size;   // row of the cache
-        elem* echo = echo_all ? echo_all + (t * a.Hkv + hd) * a.D + j0 : nullptr;
-        if constexpr (!kE2M1) {
-          Row<Tag>::store8(static_cast<elem*>(is_k ? a.k_pages : a.v_pages) + row * a.D + j0, true, x);
-          if (echo) Row<Tag>::store8(echo, vec_e, x);
-        } else {
-          const unsigned pair = 3u << (tid & 30);
-          // |fp32 value - exact value| <= err: the coefficients are off by 2^-24, products and sum
-          // rounded, 2.5 * 2^-24 of the two magnitudes; 2^-20 leaves room
-          float err = reach * 9.5367432e-7f, top = 0.f;
+      for (int c = 0; c < 4; ++c) {
+        const float z0 = x[2 * c] * per, z1 = x[2 * c + 1] * per;
+        const float w0 = fmaf(fabsf(z0), 1e-6f, room), w1 = fmaf(fabsf(z1), 1e-6f, room);
+        const uint32_t lo = codes_of(z0 - w0, z1 - w1), hi = codes_of(z0 + w0, z1 + w1);
+        // (NaN, and the sign of a zero that may be either side: not sure)
+        sure = sure && lo == hi && z0 == z0 && z1 == z1;
+        packed |= lo << (8 * c);
+      }
+      sure = __shfl_xor_sync(pair, sure, 1) && sure;
+      if (!sure)
+        packed = exact_codes<Tag>(src, j0, is_k ? a.rot : 0, a.interleaved != 0, __ldg(a.positions + t), a.inv_freq, g, sc);
+      uint8_t* pages = static_cast<uint8_t*>(is_k ? a.k_pages : a.v_pages);
+      *reinterpret_cast<uint32_t*>(pages + row * (a.D >> 1) + (j0 >> 1)) = packed;
+      if ((j0 & 15) == 0) {
+        uint8_t* bs = static_cast<uint8_t*>(is_k ? a.k_block_scales : a.v_block_scales);
+        bs[row * (a.D >> 4) + (j0 >> 4)] = (uint8_t)sc;
+      }
+      if (echo) {                                 // level * s is exact, one rounding with g
+        const float sv = e4m3_value(sc);
+        float v[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[e]));   // drops NaN
-          top = fmaxf(top, __shfl_xor_sync(pair, top, 1));
-          const float err2 = fmaxf(err, __shfl_xor_sync(pair, err, 1));
-          const float* scales = is_k ? a.k_scale : a.v_scale;
-          const float g = scales ? __ldg(scales + hd) : 1.f;
-          // the scale from both ends of its interval (the quotients are off by 2^-21 at most)
-          const float per6 = 1.f / (6.f * g), mid = top * per6;
-          const float wide = fmaf(mid, 1e-6f, err2 * per6);
-          const unsigned ends = scales_of(fmaxf(mid - wide, 0.f), mid + wide);
-          unsigned sc = ends & 0xffu;
-          const float s = e4m3_value(sc), per = s > 0.f ? 1.f / (s * g) : 0.f;
-          uint32_t packed = 0;
-          bool sure = ends == sc * 0x101u && wide <= 1e30f;
-          const float room = err * per;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const float z0 = x[2 * c] * per, z1 = x[2 * c + 1] * per;
-            const float w0 = fmaf(fabsf(z0), 1e-6f, room), w1 = fmaf(fabsf(z1), 1e-6f, room);
-            const uint32_t lo = codes_of(z0 - w0, z1 - w1), hi = codes_of(z0 + w0, z1 + w1);
-            // (NaN, and the sign of a zero that may be either side: not sure)
-            sure = sure && lo == hi && z0 == z0 && z1 == z1;
-            packed |= lo << (8 * c);
-          }
-          sure = __shfl_xor_sync(pair, sure, 1) && sure;
-          if (!sure)
-            packed = exact_codes<Tag>(src, j0, is_k ? a.rot : 0, a.interleaved != 0, __ldg(a.positions + t), a.inv_freq, g, sc);
-          uint8_t* pages = static_cast<uint8_t*>(is_k ? a.k_pages : a.v_pages);
-          *reinterpret_cast<uint32_t*>(pages + row * (a.D >> 1) + (j0 >> 1)) = packed;
-          if ((j0 & 15) == 0) {
-            uint8_t* bs = static_cast<uint8_t*>(is_k ? a.k_block_scales : a.v_block_scales);
-            bs[row * (a.D >> 4) + (j0 >> 4)] = (uint8_t)sc;
-          }
-          if (echo) {                                 // level * s is exact, one rounding with g
-            const float sv = e4m3_value(sc);
-            float v[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = e2m1_value(packed >> (4 * e)) * sv * g;
-            Row<Tag>::store8(echo, vec_e, v);
-          }
-        }
+        for (int e = 0; e < 8; ++e) v[e] = e2m1_value(packed >> (4 * e)) * sv * g;
+        Row<Tag>::store8(echo, vec_e, v);
       }
     }
   }
@@ -450,7 +459,7 @@ void launch_rows(const AppendLaunch& L, cudaStream_t stream) {
 cudaError_t launch_append(const AppendLaunch& in, cudaStream_t stream) {
   AppendLaunch L = in;
   // a row to a CTA while there are few
-  L.rows_per_cta = L.a.T <= 2 * kNumSMs ? 1 : (L.a.T <= 16 * kNumSMs ? 2 : kMaxAppendRows);
+  L.rows_per_cta = L.a.T <= 8 * kNumSMs ? 1 : kMaxAppendRows;
   if (L.a.dtype == PSPEC_BF16) launch_rows<BF16Tag>(L, stream);
   else launch_rows<F32Tag>(L, stream);
   return cudaGetLastError();
