@@ -1,12 +1,10 @@
 // append_kv.cu -- keys and values into the paged cache, rotated to their positions (one
 // launch), with the query rows rotated beside them.
 //
-// A CTA takes `rows_per_cta` rows, all their heads in one list: every thread owns the same eight
-// elements of each head that it comes to, and fetches a few heads ahead, so that the CTA is
-// bound by what the memory delivers and not by one head's latency after another (a head at a
-// time: 179 us for 15360 rows of 80 heads of 64 bf16, 25 percent padding; so: TIMES).
+// A row goes to a CTA, or to a warp when there are many: every thread owns the same eight
+// elements of each head that it comes to, and fetches a few heads ahead.
 // Partners of the half split come from the lane that holds them where a head's lanes lie in one
-// warp.  The first heads are on their way while the sines and cosines of the rows' angles are
+// warp.  The first heads are on their way while the sines and cosines of the row's angles are
 // formed, once for all heads.  Angles pos * inv_freq are formed and reduced in fp64 (positions
 // reach 10^6: an fp32 product would be off by 0.06 rad there), rotations run in fp32.
 //
@@ -15,6 +13,8 @@
 // both ends of the interval that holds the exact value, and where the ends differ (a few blocks
 // in ten thousand) the block is done again in fp64, whose borders mid * s * g (3 + 4 + 24
 // significant bits) are exact, so that ties are seen as ties.
+#include <type_traits>
+
 #include "common.cuh"
 #include "kernels.h"
 #include "plan.h"
@@ -22,8 +22,6 @@
 namespace pspec {
 
 namespace {
-
-constexpr int kMaxAppendRows = 4;        // of a CTA
 
 template <typename Tag> struct Row;
 template <> struct Row<BF16Tag> {
@@ -204,82 +202,55 @@ __device__ __noinline__ uint32_t exact_codes(const typename Tag::elem* head, int
 // How partners are found.
 enum { kAnyhow, kByLane, kInterleaved };   // the first for any rows; the others for 16-byte aligned
 
-template <typename Tag, bool kE2M1, int kMode>
+template <typename Tag, bool kE2M1, int kMode, int kTeam>
 __global__ void __launch_bounds__(kThreads, 3) append_kernel(const AppendLaunch L) {
   using elem = typename Tag::elem;
   constexpr int kRaw = Row<Tag>::kRaw, kAhead = kMode == kAnyhow ? 1 : Row<Tag>::kAhead;
-  extern __shared__ __align__(16) float2 s_cs[];      // [rows_per_cta][rot / 2] (cos, sin)
-  __shared__ long long s_row[kMaxAppendRows];         // the row's place under head 0; -1: none
+  extern __shared__ __align__(16) float2 s_all[];     // [teams][rot / 2] (cos, sin)
   const pspec_append_args& a = L.a;
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x % kTeam, team = threadIdx.x / kTeam;
   const int h = a.rot >> 1;
-  const long long t0 = (long long)blockIdx.x * L.rows_per_cta;
-  const int rows = (int)min((long long)L.rows_per_cta, a.T - t0);
+  const long long t = (long long)blockIdx.x * (kThreads / kTeam) + team;
+  float2* s_cs = s_all + team * h;
+  if (t >= a.T) return;                               // (whole teams leave)
 
-  if (tid < rows) {
-    const long long slot = __ldg(reinterpret_cast<const long long*>(a.slot_mapping) + t0 + tid);
-    long long at = -1;
-    if (slot >= 0 && slot < L.slots) {
-      const long long block = L.slots <= 0x7fffffff ? (unsigned)slot / (unsigned)a.block_size : slot / a.block_size;
-      at = block * a.Hkv * a.block_size + (slot - block * a.block_size);
-    } else if (slot != PSPEC_PADDING_SLOT_ID) {
-      set_err(a.err, PSPEC_DEVERR_BLOCK_RANGE);
-    }
-    s_row[tid] = at;
+  const long long slot = __ldg(reinterpret_cast<const long long*>(a.slot_mapping) + t);
+  if (slot < 0 || slot >= L.slots) {
+    if (tid == 0 && slot != PSPEC_PADDING_SLOT_ID) set_err(a.err, PSPEC_DEVERR_BLOCK_RANGE);
+    return;
   }
-  __syncthreads();
+  const long long block = L.slots <= 0x7fffffff ? (unsigned)slot / (unsigned)a.block_size : slot / a.block_size;
+  const long long under = block * a.Hkv * a.block_size + (slot - block * a.block_size);   // of head 0
 
   const int nl = a.D >> 3;                            // threads per head, eight elements each
-  const int groups = kThreads / nl;
+  const int groups = kTeam / nl;
   const int hg = tid / nl, j0 = (tid - hg * nl) * 8;
   const bool turns = j0 < a.rot;
   const bool low = j0 < h;                            // (half split) partners lie above
   const int from = (low ? tid + (h >> 3) : tid - (h >> 3)) & 31;
 
-  // Query heads, and key then value heads, rows x heads of them in a list: each thread has every
-  // groups-th from its hg-th on.
-  struct Cursor {
-    int r, hd, heads, step_r, step_h;
-    __device__ __forceinline__ Cursor(int at, int n, int step)
-        : r(at / n), hd(at % n), heads(n), step_r(step / n), step_h(step % n) {}
-    __device__ __forceinline__ void next() {
-      r += step_r;
-      hd += step_h;
-      if (hd >= heads) {
-        hd -= heads;
-        ++r;
-      }
-    }
-  };
-  auto there = [&](const Cursor& c) { return hg < groups && c.r < rows && s_row[c.r] >= 0; };
-  const int total_q = a.q ? rows * a.Hq : 0, total_kv = rows * 2 * a.Hkv;
-  Cursor at_q(hg, max(1, a.Hq), groups), at_kv(hg, 2 * a.Hkv, groups), ahead_q = at_q, ahead_kv = at_kv;
-  auto src_q = [&](int r, int hd) {
-    return static_cast<const elem*>(a.q) + (t0 + r) * a.q_stride + (long long)hd * a.D;
-  };
-  auto src_kv = [&](int r, int hd) {
-    return hd < a.Hkv ? static_cast<const elem*>(a.k) + (t0 + r) * a.k_stride + (long long)hd * a.D
-                      : static_cast<const elem*>(a.v) + (t0 + r) * a.v_stride + (long long)(hd - a.Hkv) * a.D;
-  };
+  // Query heads; key, then value heads: each thread has every groups-th from its hg-th on.
+  const int total_q = a.q ? a.Hq : 0, total_kv = 2 * a.Hkv;
+  const bool mine = hg < groups;
+  const elem* qs = static_cast<const elem*>(a.q) + t * a.q_stride + j0;
+  const elem* ks = static_cast<const elem*>(a.k) + t * a.k_stride + j0;
+  const elem* vs = static_cast<const elem*>(a.v) + t * a.v_stride + j0;
   auto fetch_q = [&](int i0, uint4 (&raw)[kAhead][kRaw]) {
 #pragma unroll
     for (int b = 0; b < kAhead; ++b) {
-      if (i0 + b * groups < total_q) {
-        if (there(ahead_q)) fetch8<Tag>(src_q(ahead_q.r, ahead_q.hd) + j0, kMode != kAnyhow || L.vec_q, raw[b]);
-        ahead_q.next();
-      }
+      const int hd = i0 + hg + b * groups;
+      if (mine && hd < total_q) fetch8<Tag>(qs + hd * a.D, kMode != kAnyhow || L.vec_q, raw[b]);
     }
   };
   auto fetch_kv = [&](int i0, uint4 (&raw)[kRaw]) {
-    if (i0 < total_kv) {
-      const Cursor& c = ahead_kv;
-      if (there(c)) fetch8<Tag>(src_kv(c.r, c.hd) + j0, kMode != kAnyhow || (c.hd < a.Hkv ? L.vec_k : L.vec_v), raw);
-      ahead_kv.next();
-    }
+    const int hd = i0 + hg;
+    if (mine && hd < total_kv)
+      fetch8<Tag>(hd < a.Hkv ? ks + hd * a.D : vs + (hd - a.Hkv) * a.D,
+                  kMode != kAnyhow || (hd < a.Hkv ? L.vec_k : L.vec_v), raw);
   };
-  // x turned, of a head at src in row r; the largest magnitudes that entered, added.  Every lane
+  // x turned, of the head whose part at j0 is src; the largest magnitudes that entered, added.  Every lane
   // of the warp comes here.
-  auto turn = [&](const elem* src, int r, bool ok, bool wanted, const uint4 (&raw)[kRaw], float (&x)[8]) {
+  auto turn = [&](const elem* src, bool wanted, const uint4 (&raw)[kRaw], float (&x)[8]) {
     float p[8], reach = 0.f, most = 0.f;
     if constexpr (kMode == kByLane) {
       // (the sign of the sine with the partners')
@@ -291,9 +262,9 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(const AppendLaunch 
                           __shfl_sync(0xffffffffu, raw[i].z, from) ^ flip, __shfl_sync(0xffffffffu, raw[i].w, from) ^ flip);
       values8<Tag>(o, p);
     }
-    if (!turns || !ok || !wanted) return 0.f;
+    if (!turns || !wanted) return 0.f;
     if constexpr (kMode == kByLane) {                 // whole threads turn
-      const float4* cs = reinterpret_cast<const float4*>(s_cs + r * h + (low ? j0 : j0 - h));
+      const float4* cs = reinterpret_cast<const float4*>(s_cs + (low ? j0 : j0 - h));
 #pragma unroll
       for (int e = 0; e < 8; e += 2) {
         const float4 v = cs[e >> 1];
@@ -306,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(const AppendLaunch 
 #pragma unroll
       for (int e = 0; e < 8; e += 2) {
         if (j0 + e < a.rot) {
-          const float2 v = s_cs[r * h + ((j0 + e) >> 1)];
+          const float2 v = s_cs[((j0 + e) >> 1)];
           const float u = x[e], w = x[e + 1];
           reach = fmaxf(reach, fmaxf(fabsf(u), fabsf(w)));
           x[e] = fmaf(u, v.x, -(w * v.y));
@@ -318,8 +289,8 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(const AppendLaunch 
 #pragma unroll 1
       for (int j = j0; j < min(j0 + 8, a.rot); ++j) {
         const bool under = j < h;
-        const float2 v = s_cs[r * h + (under ? j : j - h)];
-        const float u = load_scalar(src, j), w = load_scalar(src, under ? j + h : j - h);
+        const float2 v = s_cs[(under ? j : j - h)];
+        const float u = load_scalar(src, j - j0), w = load_scalar(src, (under ? j + h : j - h) - j0);
         reach = fmaxf(reach, fabsf(u));
         most = fmaxf(most, fabsf(w));
         const float y = fmaf(u, v.x, w * (under ? -v.y : v.y));
@@ -335,54 +306,50 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(const AppendLaunch 
   fetch_kv(groups, next[1]);
   fetch_q(0, raw);
 
-  for (int i = tid; i < rows * h; i += kThreads) {
-    const int r = i / h, j = i - r * h;
-    if (s_row[r] < 0) continue;
+  const double pos = (double)__ldg(a.positions + t);
+  for (int j = tid; j < h; j += kTeam) {
     double s, c;
-    turn_of((double)__ldg(a.positions + t0 + r) * (double)__ldg(a.inv_freq + j), s, c);
-    s_cs[i] = make_float2((float)c, (float)s);
+    turn_of(pos * (double)__ldg(a.inv_freq + j), s, c);
+    s_cs[j] = make_float2((float)c, (float)s);
   }
-  __syncthreads();
+  if constexpr (kTeam == 32) __syncwarp();
+  else __syncthreads();
 
+  elem* qo = static_cast<elem*>(a.q_out) + t * a.Hq * a.D + j0;
   for (int i0 = 0; i0 < total_q; i0 += kAhead * groups) {     // the same for every thread
     if (i0 > 0) fetch_q(i0, raw);
 #pragma unroll
     for (int b = 0; b < kAhead; ++b) {
-      if (i0 + b * groups >= total_q) break;
-      const bool ok = there(at_q);
-      const int r = min(at_q.r, rows - 1), hd = at_q.hd;
-      at_q.next();
+      const int hd = i0 + hg + b * groups;
+      const bool ok = mine && hd < total_q;
       float x[8];
       values8<Tag>(raw[b], x);
-      turn(src_q(r, hd), r, ok, true, raw[b], x);
-      if (ok)
-        Row<Tag>::store8(static_cast<elem*>(a.q_out) + ((t0 + r) * a.Hq + hd) * a.D + j0, kMode != kAnyhow || L.vec_qo, x);
+      turn(qs + hd * a.D, ok, raw[b], x);
+      if (ok) Row<Tag>::store8(qo + hd * a.D, kMode != kAnyhow || L.vec_qo, x);
     }
   }
 
 #pragma unroll 1
   for (int i0 = 0; i0 < total_kv; i0 += groups) {
-    const bool ok = there(at_kv), is_k = at_kv.hd < a.Hkv;
-    const int r = min(at_kv.r, rows - 1), hd = is_k ? at_kv.hd : at_kv.hd - a.Hkv;
-    const elem* src = src_kv(r, at_kv.hd);
-    at_kv.next();
+    const bool ok = mine && i0 + hg < total_kv, is_k = i0 + hg < a.Hkv;
+    const int hd = is_k ? i0 + hg : i0 + hg - a.Hkv;
+    const elem* src = (is_k ? ks : vs) + hd * a.D;
     float x[8];
     values8<Tag>(next[0], x);
-    const float reach = turn(src, r, ok, is_k, next[0], x);
+    const float reach = turn(src, ok && is_k, next[0], x);
 #pragma unroll
     for (int i = 0; i < kRaw; ++i) next[0][i] = next[1][i];
     fetch_kv(i0 + 2 * groups, next[1]);
     if (!ok) continue;
     elem* echo_all = static_cast<elem*>(is_k ? a.k_out : a.v_out);
     const bool vec_e = kMode != kAnyhow || (is_k ? L.vec_ko : L.vec_vo);
-    const long long t = t0 + r;
-    const long long row = s_row[r] + (long long)hd * a.block_size;   // row of the cache
+    const long long row = under + (long long)hd * a.block_size;      // row of the cache
     elem* echo = echo_all ? echo_all + (t * a.Hkv + hd) * a.D + j0 : nullptr;
     if constexpr (!kE2M1) {
       Row<Tag>::store8(static_cast<elem*>(is_k ? a.k_pages : a.v_pages) + row * a.D + j0, true, x);
       if (echo) Row<Tag>::store8(echo, vec_e, x);
     } else {
-      const unsigned pair = 3u << (tid & 30);
+      const unsigned pair = 3u << (threadIdx.x & 30);
       // |fp32 value - exact value| <= err: the coefficients are off by 2^-24, products and sum
       // rounded, 2.5 * 2^-24 of the two magnitudes; 2^-20 leaves room
       float err = reach * 9.5367432e-7f, top = 0.f;
@@ -412,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(const AppendLaunch 
       }
       sure = __shfl_xor_sync(pair, sure, 1) && sure;
       if (!sure)
-        packed = exact_codes<Tag>(src, j0, is_k ? a.rot : 0, a.interleaved != 0, __ldg(a.positions + t), a.inv_freq, g, sc);
+        packed = exact_codes<Tag>(src - j0, j0, is_k ? a.rot : 0, a.interleaved != 0, __ldg(a.positions + t), a.inv_freq, g, sc);
       uint8_t* pages = static_cast<uint8_t*>(is_k ? a.k_pages : a.v_pages);
       *reinterpret_cast<uint32_t*>(pages + row * (a.D >> 1) + (j0 >> 1)) = packed;
       if ((j0 & 15) == 0) {
@@ -433,8 +400,12 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(const AppendLaunch 
 template <typename Tag>
 void launch_rows(const AppendLaunch& L, cudaStream_t stream) {
   const pspec_append_args& a = L.a;
-  const unsigned grid = (unsigned)((a.T + L.rows_per_cta - 1) / L.rows_per_cta);
-  const size_t smem = (size_t)L.rows_per_cta * (a.rot / 2) * sizeof(float2);
+  // A CTA to a row while there are few, else a warp: rows then wait for nothing but their own
+  // loads (15360 rows: TEAM).
+  const bool warps = a.T > 8 * kNumSMs && a.D <= 256;
+  const int teams = warps ? kThreads / 32 : 1;
+  const unsigned grid = (unsigned)(((long long)a.T + teams - 1) / teams);
+  const size_t smem = (size_t)teams * (a.rot / 2) * sizeof(float2);
   const bool aligned = (!a.q || (L.vec_q && L.vec_qo)) && L.vec_k && L.vec_v && L.vec_ko && L.vec_vo;
   // partners in another lane: a head's lanes lie in one warp, whole threads on each side
   const int nl = a.D / 8;
@@ -442,24 +413,23 @@ void launch_rows(const AppendLaunch& L, cudaStream_t stream) {
   if (aligned && a.rot == 0) mode = kInterleaved;
   else if (aligned && a.interleaved) mode = kInterleaved;
   else if (aligned && (nl & (nl - 1)) == 0 && nl <= 32 && a.rot % 16 == 0) mode = kByLane;
-  auto go = [&](auto* fn) { fn<<<grid, kThreads, smem, stream>>>(L); };
-  if (a.cache == PSPEC_CACHE_E2M1) {
-    if (mode == kByLane) go(append_kernel<Tag, true, kByLane>);
-    else if (mode == kInterleaved) go(append_kernel<Tag, true, kInterleaved>);
-    else go(append_kernel<Tag, true, kAnyhow>);
-  } else {
-    if (mode == kByLane) go(append_kernel<Tag, false, kByLane>);
-    else if (mode == kInterleaved) go(append_kernel<Tag, false, kInterleaved>);
-    else go(append_kernel<Tag, false, kAnyhow>);
-  }
+  auto go = [&](auto* one, auto* many) {
+    if (warps) many<<<grid, kThreads, smem, stream>>>(L);
+    else one<<<grid, kThreads, smem, stream>>>(L);
+  };
+  auto pick = [&](auto e2m1) {
+    constexpr bool kE2M1 = decltype(e2m1)::value;
+    if (mode == kByLane) go(append_kernel<Tag, kE2M1, kByLane, kThreads>, append_kernel<Tag, kE2M1, kByLane, 32>);
+    else if (mode == kInterleaved) go(append_kernel<Tag, kE2M1, kInterleaved, kThreads>, append_kernel<Tag, kE2M1, kInterleaved, 32>);
+    else go(append_kernel<Tag, kE2M1, kAnyhow, kThreads>, append_kernel<Tag, kE2M1, kAnyhow, 32>);
+  };
+  if (a.cache == PSPEC_CACHE_E2M1) pick(std::true_type{});
+  else pick(std::false_type{});
 }
 
 }  // namespace
 
-cudaError_t launch_append(const AppendLaunch& in, cudaStream_t stream) {
-  AppendLaunch L = in;
-  // a row to a CTA while there are few
-  L.rows_per_cta = L.a.T <= 8 * kNumSMs ? 1 : kMaxAppendRows;
+cudaError_t launch_append(const AppendLaunch& L, cudaStream_t stream) {
   if (L.a.dtype == PSPEC_BF16) launch_rows<BF16Tag>(L, stream);
   else launch_rows<F32Tag>(L, stream);
   return cudaGetLastError();

@@ -130,7 +130,6 @@ void record_last_call(int launches, int path);
 
 struct AppendLaunch {
   pspec_append_args a;
-  int rows_per_cta;
   long long slots;                // num_blocks * block_size
   bool vec_q, vec_k, vec_v;       // rows whose eight-element groups are 16-byte aligned
   bool vec_qo, vec_ko, vec_vo;
