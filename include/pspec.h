@@ -83,6 +83,9 @@ typedef enum { PSPEC_F32 = 0, PSPEC_BF16 = 1 } pspec_dtype;
                                           infinite temperature: that filter is off (for
                                           the temperature: 1) */
 
+#define PSPEC_DEVERR_WAIT 0x80         /* a wait inside a kernel ran out (it should never):
+                                          the call's outputs are undefined */
+
 /* Row kinds written to pspec_build_args.row_kind. */
 #define PSPEC_ROW_CTX 0   /* context row: accepted token paired with its target hidden */
 #define PSPEC_ROW_NTP 1   /* next-token row: bonus token paired with h_context */

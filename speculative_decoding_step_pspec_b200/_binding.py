@@ -20,7 +20,7 @@ PSPEC_F32, PSPEC_BF16 = 0, 1
 PSPEC_DEVERR_TOKEN_RANGE, PSPEC_DEVERR_ACCEPT_RANGE = 0x1, 0x2
 PSPEC_DEVERR_BLOCK_RANGE, PSPEC_DEVERR_LAYOUT = 0x4, 0x8
 PSPEC_DEVERR_KLEN_RANGE = 0x20
-PSPEC_DEVERR_PARAM_RANGE = 0x40
+PSPEC_DEVERR_PARAM_RANGE, PSPEC_DEVERR_WAIT = 0x40, 0x80
 PSPEC_CACHE_ROWS, PSPEC_CACHE_E2M1 = 0, 1
 PSPEC_ROW_CTX, PSPEC_ROW_NTP, PSPEC_ROW_MASK, PSPEC_ROW_REJ, PSPEC_ROW_PAD = range(5)
 PSPEC_PADDING_SLOT_ID = -1

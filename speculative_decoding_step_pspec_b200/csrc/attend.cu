@@ -18,24 +18,20 @@
 // 16 (or 8) bytes of one key ARE its fragments of 8 (or 4) products, and two keys' nibbles
 // interleaved are the pairs that the product with the values wants.  Dequantised values are
 // exact in fp16: 2 significant bits of the code times 4 of the scale, between 2^-10 and 2688.
-#include "common.cuh"
-#include "kernels.h"
-#include "plan.h"
+#include "attend_common.cuh"
 
 namespace pspec {
+
+using namespace attention;
 
 namespace {
 
 constexpr int kAttWarps = 4;
 constexpr int kAttThreads = 32 * kAttWarps;
 constexpr int kStep = 16;                       // keys of one warp step
-constexpr int kUnit = kStep * kAttWarps;        // keys of one unit
+static_assert(kUnit == kStep * kAttWarps, "a step of each warp");
 constexpr int kStages = 4;
 constexpr int kAttendMaxCtas = kNumSMs * 5;
-// Probabilities are formed as 2^(x - m + kShift) and the maximum m follows only when a row
-// passes it by more than kSlack: both leave them below 2^15 (fp16 holds 65504) and far above
-// fp16's subnormals, and the outputs are rescaled rarely.
-constexpr float kShift = 7.f, kSlack = 8.f;
 constexpr float kNoMax = -1e30f;                // taken from the exponents of a row without a key
 // Persistent CTAs that fit an SM by their registers.
 constexpr int attend_ctas_per_sm(int D, bool f32, int NT) {
@@ -79,128 +75,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
   return d;
 }
 
-// Four bytes of two e2m1 codes each, as four fp16 pairs (low nibble first).
-__device__ __forceinline__ void codes_to_half(uint32_t w, uint32_t (&h)[4]) {
-  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\tcvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\tcvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
-      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
-      : "r"(w));
-}
-__device__ __forceinline__ uint32_t scales_to_half(uint32_t two) {   // two e4m3 bytes
-  uint32_t h;
-  // the maximum with zero: a NaN scale (a key that no row may see can hold anything) or a
-  // negative one counts as 0, so that a probability of zero times the value is zero
-  asm("{\n\t.reg .b16 s;\n\t.reg .b32 v;\n\tcvt.u16.u32 s, %1;\n\tcvt.rn.f16x2.e4m3x2 v, s;\n\t"
-      "max.f16x2 %0, v, %2;\n\t}" : "=r"(h) : "r"(two), "r"(0u));
-  return h;
-}
-__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
-  uint32_t d;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-  return d;
-}
-__device__ __forceinline__ float half_lo(uint32_t h) {
-  float f;
-  asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %1;\n\tcvt.f32.f16 %0, l;\n\t}" : "=f"(f) : "r"(h));
-  return f;
-}
-__device__ __forceinline__ float half_hi(uint32_t h) {
-  float f;
-  asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %1;\n\tcvt.f32.f16 %0, u;\n\t}" : "=f"(f) : "r"(h));
-  return f;
-}
-
-// The rows and keys of sequence i, made safe: a malformed offset pair has no rows, lengths
-// stay inside the block table.
-struct Seq {
-  int row0, rows, len, tiles;
-  long long units;     // of one tile
-  int err;
-};
-
-template <int kTileRows>
-__device__ __forceinline__ Seq seq_of(const pspec_attend_args& a, int i, int group) {
-  Seq s;
-  s.err = 0;
-  const int lo = __ldg(a.qsl + i), hi = __ldg(a.qsl + i + 1);
-  s.row0 = lo;
-  s.rows = hi - lo;
-  if (lo < 0 || hi < lo || hi > a.T) {
-    s.err |= PSPEC_DEVERR_LAYOUT;
-    s.row0 = s.rows = 0;
-  }
-  const long long room = (long long)a.max_blocks * a.block_size;
-  s.len = __ldg(a.seq_lens + i);
-  if (s.len < 0 || s.len > room) {
-    s.err |= PSPEC_DEVERR_BLOCK_RANGE;
-    s.len = s.len < 0 ? 0 : (int)room;
-  }
-  const long long n = (long long)s.rows * group;
-  s.tiles = (int)((n + kTileRows - 1) / kTileRows);
-  s.units = s.len == 0 ? 1 : ((long long)s.len + kUnit - 1) / kUnit;   // an empty tile is a unit too
-  return s;
-}
-
-// Row r of a tile's sequence: its token, query head and the number of keys it may see (-1: the
-// row is not computed).
-struct RowRef {
-  long long at;        // token * Hq + head
-  int limit;
-};
-
-__device__ __forceinline__ RowRef row_of(const pspec_attend_args& a, const Seq& s, int group, int h,
-                                         long long r) {
-  RowRef x{0, -1};
-  if (r >= (long long)s.rows * group) return x;
-  const int j = (int)(r / group);
-  const int t = s.row0 + j;
-  if (a.row_kind && __ldg(a.row_kind + t) >= PSPEC_ROW_REJ) return x;
-  x.at = (long long)t * a.Hq + h * group + (int)(r - (long long)j * group);
-  const int pos = __ldg(a.positions + t);
-  x.limit = pos < 0 ? 0 : min(s.len, pos == 0x7fffffff ? pos : pos + 1);
-  return x;
-}
-
-__device__ __forceinline__ void load_q2(const uint16_t* p, float& x, float& y) {
-  x = __uint_as_float((uint32_t)__ldg(reinterpret_cast<const unsigned short*>(p)) << 16);
-  y = __uint_as_float((uint32_t)__ldg(reinterpret_cast<const unsigned short*>(p) + 1) << 16);
-}
-__device__ __forceinline__ void load_q2(const float* p, float& x, float& y) {
-  x = __ldg(p);
-  y = __ldg(p + 1);
-}
-
-__device__ __forceinline__ void store_out(uint16_t* p, float4 v) {
-  uint32_t lo, hi;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(lo) : "f"(v.y), "f"(v.x));
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(v.w), "f"(v.z));
-  *reinterpret_cast<uint2*>(p) = make_uint2(lo, hi);
-}
-__device__ __forceinline__ void store_out(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
-
-// Where a key lies: its page's column of the block table and its place in the page.
-struct Walk {
-  int col, off;
-  __device__ __forceinline__ void set(long long key, int block_size) {
-    col = (int)((unsigned)key / (unsigned)block_size);
-    off = (int)((unsigned)key - (unsigned)col * (unsigned)block_size);
-  }
-  __device__ __forceinline__ void advance(int cols, int rest, int block_size) {   // by a unit
-    col += cols;
-    off += rest;
-    if (off >= block_size) {
-      off -= block_size;
-      ++col;
-    }
-  }
-};
-
 template <int D, int NT>
 struct AttendSmem {
   union {
@@ -210,9 +84,7 @@ struct AttendSmem {
   float m[kAttWarps][Shape<D, NT>::kRows];
   float l[kAttWarps][Shape<D, NT>::kRows];
   unsigned live[kAttWarps][kStages];          // which of the stage's keys exist
-  long long scan[kAttWarps];
-  int start_seq;
-  long long start_prefix;
+  ShareSmem share;
   int last;
 };
 
@@ -231,51 +103,11 @@ attend_kernel(const AttendLaunch L) {
   const int group = a.Hq / a.Hkv;
   const int cta = blockIdx.x;
 
-  // ---- the list of units: its length, and the sequence where this CTA's share begins
-  const int per = (a.B + kAttThreads - 1) / kAttThreads;
-  const int i_lo = min(a.B, tid * per), i_hi = min(a.B, i_lo + per);
-  long long mine = 0;
-  int bits = 0;
-  for (int i = i_lo; i < i_hi; ++i) {
-    const Seq s = seq_of<kTileRows>(a, i, group);
-    mine += s.units * s.tiles * a.Hkv;
-    bits |= s.err;
-  }
-  if (cta == 0) set_err(a.err, bits);
-  long long incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long n = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += n;
-  }
-  if (lane == 31) sm.scan[warp] = incl;
-  __syncthreads();
-  long long base = 0, U = 0;
-  for (int w = 0; w < kAttWarps; ++w) {
-    if (w < warp) base += sm.scan[w];
-    U += sm.scan[w];
-  }
-  const long long E = min((long long)L.ctas, U);            // CTAs with a share
-  if (cta >= E) return;
-  const long long w0 = cta * U / E, w1 = (cta + 1) * U / E;
-  {
-    long long at = base + incl - mine;
-    if (w0 >= at && w0 < at + mine) {
-      for (int i = i_lo; i < i_hi; ++i) {
-        const Seq s = seq_of<kTileRows>(a, i, group);
-        const long long n = s.units * s.tiles * a.Hkv;
-        if (w0 < at + n) {
-          sm.start_seq = i;
-          sm.start_prefix = at;
-          break;
-        }
-        at += n;
-      }
-    }
-  }
-  __syncthreads();
-  int seq = sm.start_seq;
-  long long prefix = sm.start_prefix;
+  Share share;
+  if (!share_of<kTileRows, kAttThreads>(a, group, L.ctas, sm.share, share)) return;
+  const long long U = share.U, E = share.E, w1 = share.w1;
+  int seq = share.seq;
+  long long prefix = share.prefix;
 
   const uint32_t ring = (uint32_t)__cvta_generic_to_shared(sm.ring[warp]);
   const uint8_t* ring_p = sm.ring[warp];
@@ -289,7 +121,7 @@ attend_kernel(const AttendLaunch L) {
 
   const int unit_cols = kUnit / a.block_size, unit_rest = kUnit - unit_cols * a.block_size;
 
-  long long w = w0;
+  long long w = share.w0;
   bool first = true;
   Seq s = seq_of<kTileRows>(a, seq, group);
   while (w < w1) {
@@ -633,14 +465,8 @@ attend_kernel(const AttendLaunch L) {
     float* part = L.parts + (2LL * cta + (first ? 0 : 1)) * S::kPart;
     first = false;
     const float vscale = a.v_scale ? __ldg(a.v_scale + h) : 1.f;
-    elem* out = static_cast<elem*>(a.out);
-
-    auto finish = [&](const RowRef& rr, int d, float M, float l_sum, float4 v) {
-      if (rr.limit < 0) return;
-      const float f = l_sum > 0.f ? vscale / l_sum : (l_sum == 0.f ? 0.f : l_sum);
-      store_out(out + rr.at * D + d, make_float4(v.x * f, v.y * f, v.z * f, v.w * f));
-      if (a.lse && d == 0)
-        a.lse[rr.at] = l_sum == 0.f ? -INFINITY : (M - kShift + log2f(l_sum)) * 0.69314718055994530942f;
+    auto finish = [&](const RowRef& rr, int d, float M, float sum, float4 v) {
+      finish_row<D, elem>(a, rr, d, M, sum, vscale, v);
     };
 
     for (int i = tid; i < kTileRows * (D / 4); i += kAttThreads) {
@@ -774,10 +600,12 @@ cudaError_t launch_d(const AttendLaunch& L, cudaStream_t stream) {
 
 size_t attend_counter_bytes() { return (sizeof(int) * kAttendMaxCtas + 255) / 256 * 256; }
 size_t attend_workspace_bytes() {
-  return (attend_counter_bytes() + sizeof(float) * 2 * kAttendMaxCtas * kMaxPart + 255) / 256 * 256;
+  const size_t parts = sizeof(float) * 2 * kAttendMaxCtas * kMaxPart, wide = attend_wide_part_bytes();
+  return (attend_counter_bytes() + (parts > wide ? parts : wide) + 255) / 256 * 256;
 }
 
 cudaError_t launch_attend(const AttendLaunch& L, cudaStream_t stream) {
+  if (attend_is_wide(L)) return launch_attend_wide(L, stream);
   if (L.a.dtype == PSPEC_BF16)
     return L.a.D == 64 ? launch_d<64, BF16Tag>(L, stream) : launch_d<128, BF16Tag>(L, stream);
   return L.a.D == 64 ? launch_d<64, F32Tag>(L, stream) : launch_d<128, F32Tag>(L, stream);

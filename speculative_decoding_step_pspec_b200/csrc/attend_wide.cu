@@ -1,0 +1,577 @@
+// attend_wide.cu -- attention over the 4-bit paged cache for many query rows (one launch).
+//
+// The same list of work as attend.cu's with tiles of 128 rows: a sequence's rows share a kv head's
+// keys, so each key is converted to fp16 once for 128 rows, and both products run on the fifth
+// generation's tensor cores with their sums in tensor memory.  Two CTAs to an SM, each
+//   4 warps of softmax, a thread to a row: the scores of 64 keys come out of tensor memory,
+//     become probabilities in registers and go back over them as fp16;
+//   4 warps that fetch codes a unit ahead, convert them and lay them into shared memory as the
+//     128-byte swizzled tiles that the products read, keys and values in two buffers each;
+//   1 thread that issues the products: scores of units n + 1 and n + 2 are on their way while the
+//     softmax has unit n.
+// A unit of 64 keys is 64 x 128 exponentials; 16 a clock bound a full tile's unit at 512 clocks of
+// an SM, its products (D = 64) at 256.  Warps without a live row skip theirs.
+//
+// Every wait has a limit, after which the CTA goes on without waiting, sets PSPEC_DEVERR_WAIT and
+// ends as usual.
+#include "attend_common.cuh"
+
+namespace pspec {
+
+using namespace attention;
+
+namespace {
+
+constexpr int kWideRows = 128;
+constexpr int kSoftThreads = 128, kFillThreads = 128;
+constexpr int kWideThreads = kSoftThreads + kFillThreads + 32;
+constexpr int kJoinThreads = 256;               // that join a tile's parts
+constexpr int kWideCtas = 2 * kNumSMs;
+constexpr uint32_t kTmemCols = 256;             // scores in two buffers of 64, outputs
+constexpr uint32_t kTmemOut = 128;
+constexpr long long kWaitClocks = 1ll << 31;     // about a second
+constexpr int kBatch = 32;                      // parts whose factors are held at once
+
+template <int D>
+struct Wide {
+  static constexpr int kPanels = D / 64;        // tiles are panels of 64 elements, 128 bytes a row
+  static constexpr int kQ = kPanels * kWideRows * 128;
+  static constexpr int kTile = kPanels * kUnit * 128;
+  static constexpr int kRow = D / 2;            // bytes of a key in the cache
+  static constexpr int kScaleRow = D / 16;
+  static constexpr int kChunks = D / 64;        // 16-byte pieces of a key's codes per thread
+  static constexpr int kLanes = D / 32;         // threads of a key
+  static constexpr int kStep = kFillThreads / kLanes;   // keys of one piece
+  static constexpr int kAhead = D == 64 ? 3 : 2;        // units fetched ahead
+  static constexpr long long kPart = kWideRows * (D + 2);
+};
+
+template <int D>
+struct WideSmem {
+  union {
+    uint8_t q[Wide<D>::kQ];
+    float factor[kBatch * kWideRows];
+  };
+  uint8_t k[2][Wide<D>::kTile];
+  uint8_t v[2][Wide<D>::kTile];
+  unsigned long long k_full[2], v_full[2], s_full[2], p_full[2], pv_done[2];
+  uint8_t live[2][kUnit];                       // which keys of the buffer's unit exist
+  int dead[2];                                  // the last unit of the buffer with one that does not
+  float seat[kJoinThreads];
+  float top[kWideRows];
+  int hi[4], lo[4];
+  uint32_t tmem;
+  int failed, last;
+  ShareSmem share;
+};
+
+__device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void bar_init(unsigned long long* b, int n) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(b)), "r"(n) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(unsigned long long* b) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(b)) : "memory");
+}
+__device__ __forceinline__ void bar_wait(unsigned long long* b, uint32_t parity, volatile int* failed) {
+  const uint32_t a = smem_addr(b);
+  const long long start = clock64();
+  do {
+    uint32_t done;
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(done) : "r"(a), "r"(parity) : "memory");
+    if (done || *failed) return;
+  } while (clock64() - start < kWaitClocks);
+  *failed = 1;
+}
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_commit(unsigned long long* b) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(b)) : "memory");
+}
+
+// A tile's descriptor: 128-byte swizzle, rows of 128 bytes in groups of eight 1024 bytes apart;
+// `panel`: bytes between panels of 64 elements, for an operand that is read along them.
+__device__ __forceinline__ uint64_t tile_desc(uint32_t addr, uint32_t panel) {
+  return (uint64_t)((addr & 0x3ffffu) >> 4) | (uint64_t)(panel >> 4) << 16 | (uint64_t)(1024u >> 4) << 32 | 1ull << 46 | 2ull << 61;
+}
+// fp16 operands, fp32 sums, 128 rows x N columns; transposed: B is read along its rows.
+__host__ __device__ constexpr uint32_t product_kind(int N, bool transposed) {
+  return 1u << 4 | (transposed ? 1u << 16 : 0u) | (uint32_t)(N / 8) << 17 | (128u / 16) << 24;
+}
+__device__ __forceinline__ void product(uint32_t d, uint64_t a, uint64_t b, uint32_t kind, bool add) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+               ::"r"(d), "l"(a), "l"(b), "r"(kind), "r"((int)add) : "memory");
+}
+__device__ __forceinline__ void product_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t kind, bool add) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+               ::"r"(d), "r"(a), "l"(b), "r"(kind), "r"((int)add) : "memory");
+}
+
+#define PSPEC_R8(x, o) "=r"(x[o]), "=r"(x[o + 1]), "=r"(x[o + 2]), "=r"(x[o + 3]), "=r"(x[o + 4]), "=r"(x[o + 5]), "=r"(x[o + 6]), "=r"(x[o + 7])
+#define PSPEC_W8(x, o) "r"(x[o]), "r"(x[o + 1]), "r"(x[o + 2]), "r"(x[o + 3]), "r"(x[o + 4]), "r"(x[o + 5]), "r"(x[o + 6]), "r"(x[o + 7])
+// 32 columns of the lane's row.
+__device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&x)[32]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+               "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+               : PSPEC_R8(x, 0), PSPEC_R8(x, 8), PSPEC_R8(x, 16), PSPEC_R8(x, 24) : "r"(addr));
+}
+__device__ __forceinline__ void tmem_store(uint32_t addr, const uint32_t (&x)[32]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+               "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};"
+               ::PSPEC_W8(x, 0), PSPEC_W8(x, 8), PSPEC_W8(x, 16), PSPEC_W8(x, 24), "r"(addr) : "memory");
+}
+#undef PSPEC_R8
+#undef PSPEC_W8
+#define PSPEC_RW8(x, o) "+r"(x[o]), "+r"(x[o + 1]), "+r"(x[o + 2]), "+r"(x[o + 3]), "+r"(x[o + 4]), "+r"(x[o + 5]), "+r"(x[o + 6]), "+r"(x[o + 7])
+// (x passes through, so that nothing is done with it before)
+__device__ __forceinline__ void tmem_wait_load(uint32_t (&x)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : PSPEC_RW8(x, 0), PSPEC_RW8(x, 8), PSPEC_RW8(x, 16), PSPEC_RW8(x, 24)::"memory");
+}
+#undef PSPEC_RW8
+__device__ __forceinline__ void tmem_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Byte offset of 16-byte chunk c of row r in a swizzled panel.
+__device__ __forceinline__ uint32_t chunk_at(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
+
+// 32 codes (a key's 16-byte piece `c`) with their two block scales into a tile's row.
+__device__ __forceinline__ void convert(uint8_t* tile, int panel_bytes, int row, int c, const uint4& codes, uint32_t scales) {
+  const uint32_t two = scales_to_half(scales);
+  const uint32_t f[2] = {__byte_perm(two, 0, 0x1010), __byte_perm(two, 0, 0x3232)};
+  const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
+  uint8_t* p = tile + (c >> 1) * panel_bytes;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t h[4];
+    codes_to_half(w[i], h);
+    *reinterpret_cast<uint4*>(p + chunk_at(row, (c & 1) * 4 + i)) =
+        make_uint4(hmul2(h[0], f[i >> 1]), hmul2(h[1], f[i >> 1]), hmul2(h[2], f[i >> 1]), hmul2(h[3], f[i >> 1]));
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kWideThreads, 2) attend_wide_kernel(const AttendLaunch L) {
+  using S = Wide<D>;
+  extern __shared__ uint8_t s_raw[];
+  auto& sm = *reinterpret_cast<WideSmem<D>*>(s_raw + ((1024 - (smem_addr(s_raw) & 1023)) & 1023));
+  const pspec_attend_args& a = L.a;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int group = a.Hq / a.Hkv;
+  const int cta = blockIdx.x;
+
+  Share share;
+  if (!share_of<kWideRows, kWideThreads>(a, group, L.ctas, sm.share, share)) return;
+  const long long U = share.U, E = share.E, w1 = share.w1;
+  int seq = share.seq;
+  long long prefix = share.prefix;
+
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&sm.tmem)), "r"(kTmemCols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  if (tid == 0) {
+    for (int b = 0; b < 2; ++b) {
+      bar_init(&sm.k_full[b], kFillThreads);
+      bar_init(&sm.v_full[b], kFillThreads);
+      bar_init(&sm.s_full[b], 1);
+      bar_init(&sm.p_full[b], kSoftThreads);
+      bar_init(&sm.pv_done[b], 1);
+      sm.dead[b] = -1;
+    }
+    sm.failed = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  tc_before();
+  __syncthreads();
+  tc_after();
+  const uint32_t tmem = sm.tmem;
+  volatile int* failed = &sm.failed;
+
+  int base = 0;                                 // units that the CTA has done: buffers and phases
+  long long w = share.w0;
+  bool first = true;
+  Seq s = seq_of<kWideRows>(a, seq, group);
+  while (w < w1) {
+    while (w >= prefix + s.units * s.tiles * a.Hkv) {
+      prefix += s.units * s.tiles * a.Hkv;
+      s = seq_of<kWideRows>(a, ++seq, group);
+    }
+    const long long item = (w - prefix) / s.units;
+    const long long item0 = prefix + item * s.units;          // the tile's first unit
+    const int h = (int)(item / s.tiles);
+    const long long r0 = (item - (long long)h * s.tiles) * kWideRows;
+    const long long u0 = w - item0;
+    const long long u1 = min(s.units, w1 - item0);
+    w = item0 + u1;
+
+    // ---- the rows' limits, and the query rows as fp16, power-of-two scaled into its range
+    RowRef rr{0, -1};
+    float mult = 0.f;
+    if (warp < 4) {
+      rr = row_of(a, s, group, h, r0 + tid);
+      const int hi = __reduce_max_sync(0xffffffffu, rr.limit);
+      const int lo = __reduce_min_sync(0xffffffffu, rr.limit < 0 ? 0x7fffffff : rr.limit);
+      if (lane == 0) {
+        sm.hi[warp] = hi;
+        sm.lo[warp] = lo;
+      }
+      const long long tok = rr.at / a.Hq;
+      const uint16_t* p = static_cast<const uint16_t*>(a.q) + tok * a.q_stride + (rr.at - tok * a.Hq) * D;
+      float top = 0.f;
+      if (rr.limit > 0)
+        for (int j = 0; j < D; ++j) top = fmaxf(top, fabsf(load_scalar(p, j)));
+      // 2^(14 - exponent of the row's largest element), kept within fp32's normal range
+      const int ex = (int)(__float_as_uint(top) >> 23) - 127;
+      const int up = top == 0.f || ex == 128 ? 0 : min(100, 14 - ex);
+      const float f = __uint_as_float((unsigned)(127 + up) << 23);
+      mult = a.scale * kLog2e * (a.k_scale ? __ldg(a.k_scale + h) : 1.f) * __uint_as_float((unsigned)(127 - up) << 23);
+#pragma unroll 2
+      for (int c = 0; c < D / 8; ++c) {
+        uint32_t x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float u = 0.f, v = 0.f;
+          if (rr.limit > 0) load_q2(p + 8 * c + 2 * i, u, v);
+          x[i] = pack_half(u * f, v * f);
+        }
+        *reinterpret_cast<uint4*>(sm.q + (c >> 3) * (kWideRows * 128) + chunk_at(tid, c & 7)) = make_uint4(x[0], x[1], x[2], x[3]);
+      }
+      fence_async();
+    }
+    tc_before();
+    __syncthreads();
+    tc_after();
+    const int lim_hi = max(max(sm.hi[0], sm.hi[1]), max(sm.hi[2], sm.hi[3]));
+    const int steps = max(0, (int)(min(u1, ((long long)max(lim_hi, 0) + kUnit - 1) / kUnit) - u0));
+
+    float m = -INFINITY, at = 0.f, l = 0.f;
+    if (warp < 4) {
+      // ---- softmax
+      const uint32_t mine = tmem + ((uint32_t)warp << 21);    // the warp's 32 lanes
+      const int warp_hi = sm.hi[warp], warp_lo = sm.lo[warp];
+      for (int step = 0; step < steps; ++step) {
+        const int n = base + step, b = n & 1;
+        const uint32_t parity = (n >> 1) & 1;
+        const long long k0 = (u0 + step) * kUnit;
+        bar_wait(&sm.v_full[b], parity, failed);              // sm.live and sm.dead are there
+        bar_wait(&sm.s_full[b], parity, failed);
+        __syncwarp();
+        tc_after();
+        if (k0 < warp_hi) {                                   // else no row sees the unit ...
+          const uint32_t sc = mine + b * 64;
+          uint32_t raw[2][32];
+          tmem_load(sc, raw[0]);
+          tmem_load(sc + 32, raw[1]);
+          tmem_wait_load(raw[0]);
+          tmem_wait_load(raw[1]);
+          float top = -INFINITY;
+          const bool masked = k0 + kUnit > warp_lo || sm.dead[b] == n;
+#pragma unroll
+          for (int c = 0; c < 64; ++c) {
+            float y = fmaf(__uint_as_float(raw[c >> 5][c & 31]), mult, -at);
+            if (masked && (k0 + c >= rr.limit || !sm.live[b][c])) y = -INFINITY;
+            raw[c >> 5][c & 31] = __float_as_uint(y);
+            top = fmaxf(top, y);
+          }
+          const bool grow = top > (m == -INFINITY ? -INFINITY : kShift + kSlack);
+          if (__any_sync(0xffffffffu, grow)) {
+            float f = 1.f;
+            if (grow) {
+              const float now = top + at;
+              f = ex2(m - now);
+              const float less = (now - kShift) - at;
+              m = now;
+              at = now - kShift;
+              l *= f;
+#pragma unroll
+              for (int c = 0; c < 64; ++c) raw[c >> 5][c & 31] = __float_as_uint(__uint_as_float(raw[c >> 5][c & 31]) - less);
+            }
+            if (step > 0) {
+              bar_wait(&sm.pv_done[b ^ 1], ((n - 1) >> 1) & 1, failed);
+              __syncwarp();
+              tc_after();
+#pragma unroll 1
+              for (int c = 0; c < D; c += 32) {
+                uint32_t o[32];
+                tmem_load(mine + kTmemOut + c, o);
+                tmem_wait_load(o);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                tmem_store(mine + kTmemOut + c, o);
+              }
+            }
+          }
+          uint32_t p[32];
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            const float u = ex2(__uint_as_float(raw[c >> 4][(2 * c) & 31])), v = ex2(__uint_as_float(raw[c >> 4][(2 * c + 1) & 31]));
+            sum[c & 3] += u + v;
+            p[c] = pack_half(u, v);
+          }
+          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          tmem_store(sc, p);
+          tmem_wait_store();
+        } else if (warp_hi > 0) {                             // ... and the products get zeros
+          const uint32_t z[32] = {};
+          tmem_store(mine + b * 64, z);
+          tmem_wait_store();
+        }
+        tc_before();
+        bar_arrive(&sm.p_full[b]);
+      }
+    } else if (warp < 8) {
+      // ---- keys and values into shared memory
+      const int ft = tid - kSoftThreads;
+      const int c = ft % S::kLanes, key = ft / S::kLanes;     // the thread's piece of its keys
+      const int* table = a.block_table + (long long)seq * a.max_blocks;
+      const int unit_cols = kUnit / a.block_size, unit_rest = kUnit - unit_cols * a.block_size;
+      const long long key0 = u0 * kUnit + key;
+      Walk walk[S::kChunks];
+      int blk[S::kChunks], next = 0;                          // pages of unit `next`
+      struct Codes {
+        uint4 k[S::kChunks], v[S::kChunks];
+        uint32_t ks[S::kChunks], vs[S::kChunks];
+        bool live[S::kChunks];
+      } codes[S::kAhead];
+      auto look = [&]() {
+#pragma unroll
+        for (int i = 0; i < S::kChunks; ++i)
+          blk[i] = next < steps && key0 + (long long)next * kUnit + i * S::kStep < s.len ? __ldg(table + walk[i].col) : -1;
+      };
+      // codes of the unit whose pages were looked up; the next unit's pages are looked up
+      auto fetch = [&](Codes& x) {
+#pragma unroll
+        for (int i = 0; i < S::kChunks; ++i) {
+          x.live[i] = (unsigned)blk[i] < (unsigned)a.num_blocks;
+          x.k[i] = x.v[i] = make_uint4(0, 0, 0, 0);
+          x.ks[i] = x.vs[i] = 0;
+          if (x.live[i]) {
+            const long long row = ((long long)blk[i] * a.Hkv + h) * a.block_size + walk[i].off;
+            x.k[i] = ld_stream(static_cast<const uint8_t*>(a.k_pages) + row * S::kRow + c * 16);
+            x.v[i] = ld_stream(static_cast<const uint8_t*>(a.v_pages) + row * S::kRow + c * 16);
+            x.ks[i] = __ldg(reinterpret_cast<const unsigned short*>(static_cast<const uint8_t*>(a.k_block_scales) + row * S::kScaleRow) + c);
+            x.vs[i] = __ldg(reinterpret_cast<const unsigned short*>(static_cast<const uint8_t*>(a.v_block_scales) + row * S::kScaleRow) + c);
+          }
+          walk[i].advance(unit_cols, unit_rest, a.block_size);
+        }
+        ++next;
+        look();
+      };
+#pragma unroll
+      for (int i = 0; i < S::kChunks; ++i) walk[i].set(key0 + i * S::kStep, a.block_size);
+      look();
+#pragma unroll
+      for (int j = 0; j < S::kAhead; ++j) fetch(codes[j]);
+      for (int step0 = 0; step0 < steps; step0 += S::kAhead) {
+#pragma unroll
+        for (int j = 0; j < S::kAhead; ++j) {
+          const int step = step0 + j;
+          if (step >= steps) break;
+          const int n = base + step, b = n & 1;
+          const uint32_t before = ((n >> 1) - 1) & 1;         // the buffer's previous use
+          if (n >= 2) bar_wait(&sm.s_full[b], before, failed);
+#pragma unroll
+          for (int i = 0; i < S::kChunks; ++i)
+            convert(sm.k[b], kUnit * 128, key + i * S::kStep, c, codes[j].k[i], codes[j].ks[i]);
+          fence_async();
+          bar_arrive(&sm.k_full[b]);
+          if (n >= 2) bar_wait(&sm.pv_done[b], before, failed);
+#pragma unroll
+          for (int i = 0; i < S::kChunks; ++i) {
+            const int r = key + i * S::kStep;
+            convert(sm.v[b], kUnit * 128, r, c, codes[j].v[i], codes[j].vs[i]);
+            // (only now has the softmax of the buffer's previous unit read them)
+            if (c == 0) {
+              sm.live[b][r] = codes[j].live[i];
+              if (!codes[j].live[i]) {
+                sm.dead[b] = n;
+                // a key that exists but whose page does not is hidden
+                if (key0 + (long long)step * kUnit + i * S::kStep < s.len) set_err(a.err, PSPEC_DEVERR_BLOCK_RANGE);
+              }
+            }
+          }
+          fence_async();
+          bar_arrive(&sm.v_full[b]);
+          fetch(codes[j]);
+        }
+      }
+    } else if (lane == 0 && steps > 0) {
+      // ---- products
+      auto scores = [&](int n) {
+        const int b = n & 1;
+        bar_wait(&sm.k_full[b], (n >> 1) & 1, failed);
+        tc_after();
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+          product(tmem + b * 64, tile_desc(smem_addr(sm.q) + (k >> 2) * (kWideRows * 128) + (k & 3) * 32, 16),
+                  tile_desc(smem_addr(sm.k[b]) + (k >> 2) * (kUnit * 128) + (k & 3) * 32, 16), product_kind(kUnit, false), k > 0);
+        tc_commit(&sm.s_full[b]);
+      };
+      scores(base);
+      if (steps > 1) scores(base + 1);
+      for (int step = 0; step < steps; ++step) {
+        const int n = base + step, b = n & 1;
+        const uint32_t parity = (n >> 1) & 1;
+        bar_wait(&sm.v_full[b], parity, failed);
+        bar_wait(&sm.p_full[b], parity, failed);
+        tc_after();
+#pragma unroll
+        for (int k = 0; k < kUnit / 16; ++k)
+          product_tmem(tmem + kTmemOut, tmem + b * 64 + k * 8, tile_desc(smem_addr(sm.v[b]) + k * 2048, kUnit * 128),
+                       product_kind(D, true), step > 0 || k > 0);
+        tc_commit(&sm.pv_done[b]);
+        if (step + 2 < steps) {
+          bar_wait(&sm.pv_done[b], parity, failed);           // the probabilities have been read
+          scores(n + 2);
+        }
+      }
+    }
+    __syncwarp();
+
+    // ---- the tile's outputs
+    const bool whole = u0 == 0 && u1 == s.units;
+    float* part = L.parts + (2LL * cta + (first ? 0 : 1)) * S::kPart;
+    first = false;
+    const float vscale = a.v_scale ? __ldg(a.v_scale + h) : 1.f;
+    if (warp < 4) {
+      if (steps > 0) {
+        const int n = base + steps - 1;
+        bar_wait(&sm.pv_done[n & 1], (n >> 1) & 1, failed);
+        __syncwarp();
+        tc_after();
+      }
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        uint32_t o[32];
+        tmem_load(tmem + ((uint32_t)warp << 21) + kTmemOut + c, o);
+        tmem_wait_load(o);
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {
+          // (without a key that it sees a row has no output in tensor memory)
+          float4 v = make_float4(__uint_as_float(o[i]), __uint_as_float(o[i + 1]), __uint_as_float(o[i + 2]), __uint_as_float(o[i + 3]));
+          if (m == -INFINITY && l == 0.f) v = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (whole) finish_row<D, uint16_t>(a, rr, c + i, m, l, vscale, v);
+          else *reinterpret_cast<float4*>(part + tid * D + c + i) = v;
+        }
+      }
+      if (!whole) {
+        part[kWideRows * D + tid] = m;
+        part[kWideRows * D + kWideRows + tid] = l;
+      }
+    }
+    base += steps;
+    if (!whole) {
+      // the tile's CTAs are the ones whose shares hold its first and last unit and all between
+      const long long cta_a = ((item0 + 1) * E - 1) / U;
+      const long long cta_b = ((item0 + s.units) * E - 1) / U;
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) {
+        const int n = atomicAdd(L.cnt + cta_a, 1) + 1;
+        sm.last = n == (int)(cta_b - cta_a + 1);
+        if (sm.last) L.cnt[cta_a] = 0;
+      }
+      __syncthreads();
+      if (sm.last) {
+        __threadfence();
+        // in CTA a the tile is the first of the share only when it begins there
+        const long long slot_a = 2 * cta_a + (cta_a * U / E == item0 ? 0 : 1);
+        auto part_of = [&](long long c) { return L.parts + (c == cta_a ? slot_a : 2 * c) * S::kPart; };
+        const int n = (int)(cta_b - cta_a) + 1;
+        constexpr int kSeats = kJoinThreads / kWideRows, kHeld = kWideRows * (D / 4) / kJoinThreads;
+        const bool joins = tid < kJoinThreads;
+        const int row = tid % kWideRows, place = tid / kWideRows;
+        float M = -INFINITY, sum = 0.f;
+        if (joins) {
+#pragma unroll 4
+          for (int c = place; c < n; c += kSeats) M = fmaxf(M, ld_cg(part_of(cta_a + c) + kWideRows * D + row));
+          sm.seat[tid] = M;
+        }
+        __syncthreads();
+        if (joins) {
+#pragma unroll
+          for (int i = 0; i < kSeats; ++i) M = fmaxf(M, sm.seat[i * kWideRows + row]);
+        }
+        float4 v[kHeld];
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int c0 = 0; c0 < n; c0 += kBatch) {
+          const int nb = min(kBatch, n - c0);
+          __syncthreads();
+          if (joins) {
+#pragma unroll 4
+            for (int c = place; c < nb; c += kSeats) {
+              const float* p = part_of(cta_a + c0 + c) + kWideRows * D + row;
+              const float mc = ld_cg(p), lc = ld_cg(p + kWideRows);
+              const float f = mc == -INFINITY ? 0.f : ex2(mc - M);
+              sm.factor[c * kWideRows + row] = f;
+              sum += f * lc;
+            }
+          }
+          __syncthreads();
+          if (joins) {
+            for (int c = 0; c < nb; ++c) {
+              const float4* src = reinterpret_cast<const float4*>(part_of(cta_a + c0 + c));
+#pragma unroll
+              for (int i = 0; i < kHeld; ++i) {
+                const int x = i * kJoinThreads + tid;
+                const float4 y = ld_cg(src + x);
+                const float f = sm.factor[c * kWideRows + x / (D / 4)];
+                v[i].x += f * y.x; v[i].y += f * y.y; v[i].z += f * y.z; v[i].w += f * y.w;
+              }
+            }
+          }
+        }
+        __syncthreads();
+        if (joins) {
+          sm.seat[tid] = sum;
+          if (place == 0) sm.top[row] = M;
+        }
+        __syncthreads();
+        if (joins) {
+#pragma unroll
+          for (int i = 0; i < kHeld; ++i) {
+            const int x = i * kJoinThreads + tid, r = x / (D / 4);
+            float total = 0.f;
+#pragma unroll
+            for (int p = 0; p < kSeats; ++p) total += sm.seat[p * kWideRows + r];
+            finish_row<D, uint16_t>(a, row_of(a, s, group, h, r0 + r), (x - r * (D / 4)) * 4, sm.top[r], total, vscale, v[i]);
+          }
+        }
+      }
+    }
+    tc_before();
+    __syncthreads();                                          // the tile's memory is free again
+    tc_after();
+  }
+  if (tid == 0 && sm.failed) set_err(a.err, PSPEC_DEVERR_WAIT);
+  if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
+}
+
+template <int D>
+cudaError_t launch_wide(AttendLaunch L, cudaStream_t stream) {
+  constexpr int smem = sizeof(WideSmem<D>) + 1024;
+  static_assert(2 * (smem + 1024) <= 227 * 1024, "two CTAs to an SM");
+  auto* fn = attend_wide_kernel<D>;
+  const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  L.ctas = kWideCtas;
+  fn<<<L.ctas, kWideThreads, smem, stream>>>(L);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t attend_wide_part_bytes() { return sizeof(float) * 2 * kWideCtas * Wide<128>::kPart; }
+
+bool attend_is_wide(const AttendLaunch& L) {
+  const long long rows = ((long long)L.a.T * (L.a.Hq / L.a.Hkv) + L.a.B - 1) / L.a.B;
+  return L.a.dtype == PSPEC_BF16 && rows > 32;
+}
+
+cudaError_t launch_attend_wide(const AttendLaunch& L, cudaStream_t stream) {
+  return L.a.D == 64 ? launch_wide<64>(L, stream) : launch_wide<128>(L, stream);
+}
+
+}  // namespace pspec

@@ -143,6 +143,9 @@ struct AttendLaunch {
   float* parts;                   // [2 * kAttendMaxCtas] partial tiles
 };
 cudaError_t launch_attend(const AttendLaunch& L, cudaStream_t stream);
+bool attend_is_wide(const AttendLaunch& L);              // many rows: tiles of 128 (attend_wide.cu)
+cudaError_t launch_attend_wide(const AttendLaunch& L, cudaStream_t stream);
+size_t attend_wide_part_bytes();
 size_t attend_workspace_bytes();
 size_t attend_counter_bytes();    // the counters sit at the workspace's start
 
