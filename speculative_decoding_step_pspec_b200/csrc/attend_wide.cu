@@ -55,7 +55,7 @@ struct WideSmem {
   uint8_t k[2][Wide<D>::kTile];
   uint8_t v[2][Wide<D>::kTile];
   unsigned long long k_full[2], v_full[2], s_full[2], p_full[2], pv_done[2];
-  uint8_t live[2][kUnit];                       // which keys of the buffer's unit exist
+  alignas(8) uint8_t live[2][kUnit];                       // which keys of the buffer's unit exist
   int dead[2];                                  // the last unit of the buffer with one that does not
   float seat[kJoinThreads];
   float top[kWideRows];
@@ -264,15 +264,28 @@ __global__ void __launch_bounds__(kWideThreads, 2) attend_wide_kernel(const Atte
           tmem_load(sc + 32, raw[1]);
           tmem_wait_load(raw[0]);
           tmem_wait_load(raw[1]);
-          float top = -INFINITY;
-          const bool masked = k0 + kUnit > warp_lo || sm.dead[b] == n;
 #pragma unroll
-          for (int c = 0; c < 64; ++c) {
-            float y = fmaf(__uint_as_float(raw[c >> 5][c & 31]), mult, -at);
-            if (masked && (k0 + c >= rr.limit || !sm.live[b][c])) y = -INFINITY;
-            raw[c >> 5][c & 31] = __float_as_uint(y);
-            top = fmaxf(top, y);
+          for (int c = 0; c < 64; ++c)
+            raw[c >> 5][c & 31] = __float_as_uint(fmaf(__uint_as_float(raw[c >> 5][c & 31]), mult, -at));
+          if (k0 + kUnit > warp_lo || sm.dead[b] == n) {      // some key is hidden from some row
+            const int left = (int)min((long long)kUnit, rr.limit - k0);
+            unsigned long long seen = left <= 0 ? 0ull : ~0ull >> (kUnit - left);
+            unsigned long long there = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {                     // a byte of 0 or 1 per key: eight to bits
+              const unsigned long long x = *reinterpret_cast<const unsigned long long*>(&sm.live[b][8 * i]);
+              there |= ((x * 0x0102040810204080ull) >> 56) << (8 * i);
+            }
+            seen &= there;
+#pragma unroll
+            for (int c = 0; c < 64; ++c)
+              if (!(seen >> c & 1)) raw[c >> 5][c & 31] = __float_as_uint(-INFINITY);
           }
+          float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int c = 0; c < 64; c += 2)
+            tops[c >> 1 & 3] = fmax3(tops[c >> 1 & 3], __uint_as_float(raw[c >> 5][c & 31]), __uint_as_float(raw[c >> 5][(c + 1) & 31]));
+          const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
           const bool grow = top > (m == -INFINITY ? -INFINITY : kShift + kSlack);
           if (__any_sync(0xffffffffu, grow)) {
             float f = 1.f;
