@@ -72,16 +72,25 @@ __device__ __forceinline__ void bar_init(unsigned long long* b, int n) {
 __device__ __forceinline__ void bar_arrive(unsigned long long* b) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(b)) : "memory");
 }
+__device__ __forceinline__ bool bar_done(uint32_t a, uint32_t parity) {
+  uint32_t done;
+  asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(done) : "r"(a), "r"(parity) : "memory");
+  return done != 0;
+}
+__device__ __noinline__ void bar_wait_long(uint32_t a, uint32_t parity, volatile int* failed) {
+  const long long start = clock64();
+  while (!bar_done(a, parity)) {
+    if (*failed) return;
+    if (clock64() - start > kWaitClocks) *failed = 1;
+  }
+}
 __device__ __forceinline__ void bar_wait(unsigned long long* b, uint32_t parity, volatile int* failed) {
   const uint32_t a = smem_addr(b);
-  const long long start = clock64();
-  do {
-    uint32_t done;
-    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-                 : "=r"(done) : "r"(a), "r"(parity) : "memory");
-    if (done || *failed) return;
-  } while (clock64() - start < kWaitClocks);
-  *failed = 1;
+#pragma unroll 1
+  for (int i = 0; i < 8; ++i)
+    if (bar_done(a, parity)) return;
+  bar_wait_long(a, parity, failed);
 }
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -259,17 +268,12 @@ __global__ void __launch_bounds__(kWideThreads, 2) attend_wide_kernel(const Atte
         tc_after();
         if (k0 < warp_hi) {                                   // else no row sees the unit ...
           const uint32_t sc = mine + b * 64;
-          uint32_t raw[2][32];
-          tmem_load(sc, raw[0]);
-          tmem_load(sc + 32, raw[1]);
-          tmem_wait_load(raw[0]);
-          tmem_wait_load(raw[1]);
-#pragma unroll
-          for (int c = 0; c < 64; ++c)
-            raw[c >> 5][c & 31] = __float_as_uint(fmaf(__uint_as_float(raw[c >> 5][c & 31]), mult, -at));
-          if (k0 + kUnit > warp_lo || sm.dead[b] == n) {      // some key is hidden from some row
+          // some key is hidden from some row: which ones this row sees
+          const bool masked = k0 + kUnit > warp_lo || sm.dead[b] == n;
+          unsigned long long seen = 0;
+          if (masked) {
             const int left = (int)min((long long)kUnit, rr.limit - k0);
-            unsigned long long seen = left <= 0 ? 0ull : ~0ull >> (kUnit - left);
+            seen = left <= 0 ? 0ull : ~0ull >> (kUnit - left);
             unsigned long long there = 0;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {                     // a byte of 0 or 1 per key: eight to bits
@@ -277,27 +281,47 @@ __global__ void __launch_bounds__(kWideThreads, 2) attend_wide_kernel(const Atte
               there |= ((x * 0x0102040810204080ull) >> 56) << (8 * i);
             }
             seen &= there;
-#pragma unroll
-            for (int c = 0; c < 64; ++c)
-              if (!(seen >> c & 1)) raw[c >> 5][c & 31] = __float_as_uint(-INFINITY);
           }
-          float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          // probabilities by the maximum so far; where one passes the slack, once more by the new
+          uint32_t p[32];
+          float sum[4], top;
+          auto pass = [&]() {
+            float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            sum[0] = sum[1] = sum[2] = sum[3] = 0.f;
 #pragma unroll
-          for (int c = 0; c < 64; c += 2)
-            tops[c >> 1 & 3] = fmax3(tops[c >> 1 & 3], __uint_as_float(raw[c >> 5][c & 31]), __uint_as_float(raw[c >> 5][(c + 1) & 31]));
-          const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+            for (int half = 0; half < 2; ++half) {
+              uint32_t x[32];
+              tmem_load(sc + 32 * half, x);
+              tmem_wait_load(x);
+#pragma unroll
+              for (int c = 0; c < 32; ++c) x[c] = __float_as_uint(fmaf(__uint_as_float(x[c]), mult, -at));
+              if (masked) {
+                const uint32_t bits = (uint32_t)(seen >> (32 * half));
+#pragma unroll
+                for (int c = 0; c < 32; ++c)
+                  if (!(bits >> c & 1)) x[c] = __float_as_uint(-INFINITY);
+              }
+#pragma unroll
+              for (int c = 0; c < 32; c += 2) {
+                const float y = __uint_as_float(x[c]), z = __uint_as_float(x[c + 1]);
+                tops[c >> 1 & 3] = fmax3(tops[c >> 1 & 3], y, z);
+                const float u = ex2(y), v = ex2(z);
+                sum[c >> 1 & 3] += u + v;
+                p[16 * half + (c >> 1)] = pack_half(u, v);
+              }
+            }
+            top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+          };
+          pass();
           const bool grow = top > (m == -INFINITY ? -INFINITY : kShift + kSlack);
           if (__any_sync(0xffffffffu, grow)) {
             float f = 1.f;
             if (grow) {
               const float now = top + at;
               f = ex2(m - now);
-              const float less = (now - kShift) - at;
               m = now;
               at = now - kShift;
               l *= f;
-#pragma unroll
-              for (int c = 0; c < 64; ++c) raw[c >> 5][c & 31] = __float_as_uint(__uint_as_float(raw[c >> 5][c & 31]) - less);
             }
             if (step > 0) {
               bar_wait(&sm.pv_done[b ^ 1], ((n - 1) >> 1) & 1, failed);
@@ -313,14 +337,7 @@ __global__ void __launch_bounds__(kWideThreads, 2) attend_wide_kernel(const Atte
                 tmem_store(mine + kTmemOut + c, o);
               }
             }
-          }
-          uint32_t p[32];
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            const float u = ex2(__uint_as_float(raw[c >> 4][(2 * c) & 31])), v = ex2(__uint_as_float(raw[c >> 4][(2 * c + 1) & 31]));
-            sum[c & 3] += u + v;
-            p[c] = pack_half(u, v);
+            pass();
           }
           l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
           tmem_store(sc, p);
@@ -347,6 +364,11 @@ __global__ void __launch_bounds__(kWideThreads, 2) attend_wide_kernel(const Atte
         uint32_t ks[S::kChunks], vs[S::kChunks];
         bool live[S::kChunks];
       } codes[S::kAhead];
+      const uint8_t* kp = static_cast<const uint8_t*>(a.k_pages) + c * 16;
+      const uint8_t* vp = static_cast<const uint8_t*>(a.v_pages) + c * 16;
+      const uint8_t* ksp = static_cast<const uint8_t*>(a.k_block_scales) + c * 2;
+      const uint8_t* vsp = static_cast<const uint8_t*>(a.v_block_scales) + c * 2;
+      const long long page = (long long)a.Hkv * a.block_size, head = (long long)h * a.block_size;
       auto look = [&]() {
 #pragma unroll
         for (int i = 0; i < S::kChunks; ++i)
@@ -360,11 +382,11 @@ __global__ void __launch_bounds__(kWideThreads, 2) attend_wide_kernel(const Atte
           x.k[i] = x.v[i] = make_uint4(0, 0, 0, 0);
           x.ks[i] = x.vs[i] = 0;
           if (x.live[i]) {
-            const long long row = ((long long)blk[i] * a.Hkv + h) * a.block_size + walk[i].off;
-            x.k[i] = ld_stream(static_cast<const uint8_t*>(a.k_pages) + row * S::kRow + c * 16);
-            x.v[i] = ld_stream(static_cast<const uint8_t*>(a.v_pages) + row * S::kRow + c * 16);
-            x.ks[i] = __ldg(reinterpret_cast<const unsigned short*>(static_cast<const uint8_t*>(a.k_block_scales) + row * S::kScaleRow) + c);
-            x.vs[i] = __ldg(reinterpret_cast<const unsigned short*>(static_cast<const uint8_t*>(a.v_block_scales) + row * S::kScaleRow) + c);
+            const long long row = blk[i] * page + (head + walk[i].off);
+            x.k[i] = ld_stream(kp + row * S::kRow);
+            x.v[i] = ld_stream(vp + row * S::kRow);
+            x.ks[i] = __ldg(reinterpret_cast<const unsigned short*>(ksp + row * S::kScaleRow));
+            x.vs[i] = __ldg(reinterpret_cast<const unsigned short*>(vsp + row * S::kScaleRow));
           }
           walk[i].advance(unit_cols, unit_rest, a.block_size);
         }
@@ -411,14 +433,17 @@ __global__ void __launch_bounds__(kWideThreads, 2) attend_wide_kernel(const Atte
       }
     } else if (lane == 0 && steps > 0) {
       // ---- products
+      const uint64_t qd = tile_desc(smem_addr(sm.q), 16), kd = tile_desc(smem_addr(sm.k[0]), 16),
+                     vd = tile_desc(smem_addr(sm.v[0]), kUnit * 128);
       auto scores = [&](int n) {
         const int b = n & 1;
+        const uint64_t kb = kd + b * (S::kTile >> 4);
         bar_wait(&sm.k_full[b], (n >> 1) & 1, failed);
         tc_after();
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
-          product(tmem + b * 64, tile_desc(smem_addr(sm.q) + (k >> 2) * (kWideRows * 128) + (k & 3) * 32, 16),
-                  tile_desc(smem_addr(sm.k[b]) + (k >> 2) * (kUnit * 128) + (k & 3) * 32, 16), product_kind(kUnit, false), k > 0);
+          product(tmem + b * 64, qd + ((k >> 2) * (kWideRows * 128) + (k & 3) * 32 >> 4), kb + ((k >> 2) * (kUnit * 128) + (k & 3) * 32 >> 4),
+                  product_kind(kUnit, false), k > 0);
         tc_commit(&sm.s_full[b]);
       };
       scores(base);
@@ -431,7 +456,7 @@ __global__ void __launch_bounds__(kWideThreads, 2) attend_wide_kernel(const Atte
         tc_after();
 #pragma unroll
         for (int k = 0; k < kUnit / 16; ++k)
-          product_tmem(tmem + kTmemOut, tmem + b * 64 + k * 8, tile_desc(smem_addr(sm.v[b]) + k * 2048, kUnit * 128),
+          product_tmem(tmem + kTmemOut, tmem + b * 64 + k * 8, vd + (b * S::kTile + k * 2048 >> 4),
                        product_kind(D, true), step > 0 || k > 0);
         tc_commit(&sm.pv_done[b]);
         if (step + 2 < steps) {
