@@ -3,14 +3,18 @@
 // The same list of work as attend.cu's with tiles of 128 rows: a sequence's rows share a kv head's
 // keys, so each key is converted to fp16 once for 128 rows, and both products run on the fifth
 // generation's tensor cores with their sums in tensor memory.  Two CTAs to an SM, each
-//   4 warps of softmax, a thread to a row: the scores of 64 keys come out of tensor memory,
-//     become probabilities in registers and go back over them as fp16;
-//   4 warps that fetch codes a unit ahead, convert them and lay them into shared memory as the
-//     128-byte swizzled tiles that the products read, keys and values in two buffers each;
-//   1 thread that issues the products: scores of units n + 1 and n + 2 are on their way while the
+//   8 warps of softmax, two threads to a row: the scores of 64 keys come out of tensor memory,
+//     become probabilities in registers and go back over them as fp16; the two threads of a row
+//     agree on its maximum, which moves rarely;
+//   4 warps each for the keys and the values: codes are fetched some units ahead, converted and
+//     laid into shared memory as the 128-byte swizzled tiles that the products read, two buffers
+//     each;
+//   1 warp that issues the products: scores of units n + 1 and n + 2 are on their way while the
 //     softmax has unit n.
 // A unit of 64 keys is 64 x 128 exponentials; 16 a clock bound a full tile's unit at 512 clocks of
-// an SM, its products (D = 64) at 256.  Warps without a live row skip theirs.
+// an SM, its products (D = 64) at 256.  Latency is what costs: with half the warps for each role
+// a unit took 2350 clocks of a CTA, the instructions of each one after another.  Warps without a
+// live row skip theirs.
 //
 // Every wait has a limit, after which the CTA goes on without waiting, sets PSPEC_DEVERR_WAIT and
 // ends as usual.
@@ -23,8 +27,8 @@ using namespace attention;
 namespace {
 
 constexpr int kWideRows = 128;
-constexpr int kSoftThreads = 128, kFillThreads = 128;
-constexpr int kWideThreads = kSoftThreads + kFillThreads + 32;
+constexpr int kSoftThreads = 256, kFillThreads = 128;     // fillers: of keys, and of values
+constexpr int kWideThreads = kSoftThreads + 2 * kFillThreads + 32;
 constexpr int kJoinThreads = 256;               // that join a tile's parts
 constexpr int kWideCtas = 2 * kNumSMs;
 constexpr uint32_t kTmemCols = 256;             // scores in two buffers of 64, outputs
@@ -42,7 +46,7 @@ struct Wide {
   static constexpr int kChunks = D / 64;        // 16-byte pieces of a key's codes per thread
   static constexpr int kLanes = D / 32;         // threads of a key
   static constexpr int kStep = kFillThreads / kLanes;   // keys of one piece
-  static constexpr int kAhead = D == 64 ? 3 : 2;        // units fetched ahead
+  static constexpr int kAhead = D == 64 ? 4 : 2;        // units fetched ahead
   static constexpr long long kPart = kWideRows * (D + 2);
 };
 
@@ -55,8 +59,9 @@ struct WideSmem {
   uint8_t k[2][Wide<D>::kTile];
   uint8_t v[2][Wide<D>::kTile];
   unsigned long long k_full[2], v_full[2], s_full[2], p_full[2], pv_done[2];
-  alignas(8) uint8_t live[2][kUnit];                       // which keys of the buffer's unit exist
-  int dead[2];                                  // the last unit of the buffer with one that does not
+  // of four units, for their keys may be laid before the softmax of the second last has read them
+  alignas(8) uint8_t live[4][kUnit];            // which of the keys exist
+  int dead[4];                                  // the last unit here with one that does not
   float seat[kJoinThreads];
   float top[kWideRows];
   int hi[4], lo[4];
@@ -117,28 +122,40 @@ __device__ __forceinline__ void product_tmem(uint32_t d, uint32_t a, uint64_t b,
                ::"r"(d), "r"(a), "l"(b), "r"(kind), "r"((int)add) : "memory");
 }
 
-#define PSPEC_R8(x, o) "=r"(x[o]), "=r"(x[o + 1]), "=r"(x[o + 2]), "=r"(x[o + 3]), "=r"(x[o + 4]), "=r"(x[o + 5]), "=r"(x[o + 6]), "=r"(x[o + 7])
-#define PSPEC_W8(x, o) "r"(x[o]), "r"(x[o + 1]), "r"(x[o + 2]), "r"(x[o + 3]), "r"(x[o + 4]), "r"(x[o + 5]), "r"(x[o + 6]), "r"(x[o + 7])
-// 32 columns of the lane's row.
-__device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&x)[32]) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-               "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-               : PSPEC_R8(x, 0), PSPEC_R8(x, 8), PSPEC_R8(x, 16), PSPEC_R8(x, 24) : "r"(addr));
+// 16 columns of the lane's row.
+__device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&x)[16]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+               : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]), "=r"(x[6]), "=r"(x[7]),
+                 "=r"(x[8]), "=r"(x[9]), "=r"(x[10]), "=r"(x[11]), "=r"(x[12]), "=r"(x[13]), "=r"(x[14]), "=r"(x[15])
+               : "r"(addr));
 }
-__device__ __forceinline__ void tmem_store(uint32_t addr, const uint32_t (&x)[32]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-               "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};"
-               ::PSPEC_W8(x, 0), PSPEC_W8(x, 8), PSPEC_W8(x, 16), PSPEC_W8(x, 24), "r"(addr) : "memory");
+__device__ __forceinline__ void tmem_store(uint32_t addr, const uint32_t (&x)[16]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};"
+               ::"r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7]),
+                 "r"(x[8]), "r"(x[9]), "r"(x[10]), "r"(x[11]), "r"(x[12]), "r"(x[13]), "r"(x[14]), "r"(x[15]),
+                 "r"(addr) : "memory");
 }
-#undef PSPEC_R8
-#undef PSPEC_W8
-#define PSPEC_RW8(x, o) "+r"(x[o]), "+r"(x[o + 1]), "+r"(x[o + 2]), "+r"(x[o + 3]), "+r"(x[o + 4]), "+r"(x[o + 5]), "+r"(x[o + 6]), "+r"(x[o + 7])
 // (x passes through, so that nothing is done with it before)
-__device__ __forceinline__ void tmem_wait_load(uint32_t (&x)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" : PSPEC_RW8(x, 0), PSPEC_RW8(x, 8), PSPEC_RW8(x, 16), PSPEC_RW8(x, 24)::"memory");
+__device__ __forceinline__ void tmem_wait_load(uint32_t (&x)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(x[0]), "+r"(x[1]), "+r"(x[2]), "+r"(x[3]), "+r"(x[4]), "+r"(x[5]), "+r"(x[6]), "+r"(x[7]),
+                 "+r"(x[8]), "+r"(x[9]), "+r"(x[10]), "+r"(x[11]), "+r"(x[12]), "+r"(x[13]), "+r"(x[14]), "+r"(x[15])
+               ::"memory");
 }
-#undef PSPEC_RW8
 __device__ __forceinline__ void tmem_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// The two warps that share 32 rows: meet, and whether a lane of either says so.
+__device__ __forceinline__ bool pair_any(int pair, bool x) {
+  int r;
+  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbarrier.cta.red.or.aligned.pred q, %2, 64, p;\n\t"
+               "selp.b32 %0, 1, 0, q;\n\t}" : "=r"(r) : "r"((int)x), "r"(pair + 1) : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ bool elected() {
+  int r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
 
 // Byte offset of 16-byte chunk c of row r in a swizzled panel.
 __device__ __forceinline__ uint32_t chunk_at(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
@@ -185,7 +202,7 @@ __global__ void __launch_bounds__(kWideThreads, 2) attend_wide_kernel(const Atte
       bar_init(&sm.s_full[b], 1);
       bar_init(&sm.p_full[b], kSoftThreads);
       bar_init(&sm.pv_done[b], 1);
-      sm.dead[b] = -1;
+      sm.dead[b] = sm.dead[b + 2] = -1;
     }
     sm.failed = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -214,36 +231,50 @@ __global__ void __launch_bounds__(kWideThreads, 2) attend_wide_kernel(const Atte
     w = item0 + u1;
 
     // ---- the rows' limits, and the query rows as fp16, power-of-two scaled into its range
+    const int row = tid & (kWideRows - 1), half = tid / kWideRows;   // (softmax threads)
     RowRef rr{0, -1};
     float mult = 0.f;
-    if (warp < 4) {
-      rr = row_of(a, s, group, h, r0 + tid);
+    if (warp < 8) {
+      rr = row_of(a, s, group, h, r0 + row);
       const int hi = __reduce_max_sync(0xffffffffu, rr.limit);
       const int lo = __reduce_min_sync(0xffffffffu, rr.limit < 0 ? 0x7fffffff : rr.limit);
-      if (lane == 0) {
+      if (lane == 0 && warp < 4) {
         sm.hi[warp] = hi;
         sm.lo[warp] = lo;
       }
       const long long tok = rr.at / a.Hq;
       const uint16_t* p = static_cast<const uint16_t*>(a.q) + tok * a.q_stride + (rr.at - tok * a.Hq) * D;
+      const bool vec = (reinterpret_cast<uintptr_t>(a.q) & 15) == 0 && a.q_stride % 8 == 0;
+      auto load = [&](int c, float (&x)[8]) {
+        if (rr.limit <= 0) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[i] = 0.f;
+        } else if (vec) {
+          unpack(__ldg(reinterpret_cast<const uint4*>(p) + c), x, BF16Tag{});
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[i] = load_scalar(p, 8 * c + i);
+        }
+      };
       float top = 0.f;
-      if (rr.limit > 0)
-        for (int j = 0; j < D; ++j) top = fmaxf(top, fabsf(load_scalar(p, j)));
+#pragma unroll 4
+      for (int c = 0; c < D / 8; ++c) {
+        float x[8];
+        load(c, x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[i]));
+      }
       // 2^(14 - exponent of the row's largest element), kept within fp32's normal range
       const int ex = (int)(__float_as_uint(top) >> 23) - 127;
       const int up = top == 0.f || ex == 128 ? 0 : min(100, 14 - ex);
       const float f = __uint_as_float((unsigned)(127 + up) << 23);
       mult = a.scale * kLog2e * (a.k_scale ? __ldg(a.k_scale + h) : 1.f) * __uint_as_float((unsigned)(127 - up) << 23);
 #pragma unroll 2
-      for (int c = 0; c < D / 8; ++c) {
-        uint32_t x[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float u = 0.f, v = 0.f;
-          if (rr.limit > 0) load_q2(p + 8 * c + 2 * i, u, v);
-          x[i] = pack_half(u * f, v * f);
-        }
-        *reinterpret_cast<uint4*>(sm.q + (c >> 3) * (kWideRows * 128) + chunk_at(tid, c & 7)) = make_uint4(x[0], x[1], x[2], x[3]);
+      for (int c = half * (D / 16); c < (half + 1) * (D / 16); ++c) {
+        float x[8];
+        load(c, x);
+        *reinterpret_cast<uint4*>(sm.q + (c >> 3) * (kWideRows * 128) + chunk_at(row, c & 7)) =
+            make_uint4(pack_half(x[0] * f, x[1] * f), pack_half(x[2] * f, x[3] * f), pack_half(x[4] * f, x[5] * f), pack_half(x[6] * f, x[7] * f));
       }
       fence_async();
     }
@@ -254,69 +285,68 @@ __global__ void __launch_bounds__(kWideThreads, 2) attend_wide_kernel(const Atte
     const int steps = max(0, (int)(min(u1, ((long long)max(lim_hi, 0) + kUnit - 1) / kUnit) - u0));
 
     float m = -INFINITY, at = 0.f, l = 0.f;
-    if (warp < 4) {
+    if (warp < 8) {
       // ---- softmax
-      const uint32_t mine = tmem + ((uint32_t)warp << 21);    // the warp's 32 lanes
-      const int warp_hi = sm.hi[warp], warp_lo = sm.lo[warp];
+      const uint32_t mine = tmem + ((uint32_t)(warp & 3) << 21);   // the warp's 32 lanes
+      const int warp_hi = sm.hi[warp & 3], warp_lo = sm.lo[warp & 3];
       for (int step = 0; step < steps; ++step) {
         const int n = base + step, b = n & 1;
-        const uint32_t parity = (n >> 1) & 1;
         const long long k0 = (u0 + step) * kUnit;
-        bar_wait(&sm.v_full[b], parity, failed);              // sm.live and sm.dead are there
-        bar_wait(&sm.s_full[b], parity, failed);
+        const uint32_t sc = mine + b * 64 + half * 32;        // the thread's 32 keys
+        bar_wait(&sm.s_full[b], (n >> 1) & 1, failed);
         __syncwarp();
         tc_after();
         if (k0 < warp_hi) {                                   // else no row sees the unit ...
-          const uint32_t sc = mine + b * 64;
           // some key is hidden from some row: which ones this row sees
-          const bool masked = k0 + kUnit > warp_lo || sm.dead[b] == n;
-          unsigned long long seen = 0;
+          const bool masked = k0 + kUnit > warp_lo || sm.dead[n & 3] == n;
+          uint32_t seen = 0;
           if (masked) {
-            const int left = (int)min((long long)kUnit, rr.limit - k0);
-            seen = left <= 0 ? 0ull : ~0ull >> (kUnit - left);
-            unsigned long long there = 0;
+            const int left = (int)max(0LL, min(32LL, rr.limit - k0 - half * 32));
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {                     // a byte of 0 or 1 per key: eight to bits
-              const unsigned long long x = *reinterpret_cast<const unsigned long long*>(&sm.live[b][8 * i]);
-              there |= ((x * 0x0102040810204080ull) >> 56) << (8 * i);
+            for (int i = 0; i < 4; ++i) {                     // a byte of 0 or 1 per key: eight to bits
+              const unsigned long long x = *reinterpret_cast<const unsigned long long*>(&sm.live[n & 3][half * 32 + 8 * i]);
+              seen |= (uint32_t)((x * 0x0102040810204080ull) >> 56) << (8 * i);
             }
-            seen &= there;
+            seen &= left == 0 ? 0u : 0xffffffffu >> (32 - left);
           }
           // probabilities by the maximum so far; where one passes the slack, once more by the new
-          uint32_t p[32];
-          float sum[4], top;
+          uint32_t p[16];
+          float sum[2], top;
           auto pass = [&]() {
-            float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-            sum[0] = sum[1] = sum[2] = sum[3] = 0.f;
+            float tops[2] = {-INFINITY, -INFINITY};
+            sum[0] = sum[1] = 0.f;
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              uint32_t x[32];
-              tmem_load(sc + 32 * half, x);
+            for (int part = 0; part < 2; ++part) {
+              uint32_t x[16];
+              tmem_load(sc + 16 * part, x);
               tmem_wait_load(x);
 #pragma unroll
-              for (int c = 0; c < 32; ++c) x[c] = __float_as_uint(fmaf(__uint_as_float(x[c]), mult, -at));
+              for (int c = 0; c < 16; ++c) x[c] = __float_as_uint(fmaf(__uint_as_float(x[c]), mult, -at));
               if (masked) {
-                const uint32_t bits = (uint32_t)(seen >> (32 * half));
+                const uint32_t bits = seen >> (16 * part);
 #pragma unroll
-                for (int c = 0; c < 32; ++c)
+                for (int c = 0; c < 16; ++c)
                   if (!(bits >> c & 1)) x[c] = __float_as_uint(-INFINITY);
               }
 #pragma unroll
-              for (int c = 0; c < 32; c += 2) {
+              for (int c = 0; c < 16; c += 2) {
                 const float y = __uint_as_float(x[c]), z = __uint_as_float(x[c + 1]);
-                tops[c >> 1 & 3] = fmax3(tops[c >> 1 & 3], y, z);
+                tops[c >> 1 & 1] = fmax3(tops[c >> 1 & 1], y, z);
                 const float u = ex2(y), v = ex2(z);
-                sum[c >> 1 & 3] += u + v;
-                p[16 * half + (c >> 1)] = pack_half(u, v);
+                sum[c >> 1 & 1] += u + v;
+                p[8 * part + (c >> 1)] = pack_half(u, v);
               }
             }
-            top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+            top = fmaxf(tops[0], tops[1]);
           };
           pass();
-          const bool grow = top > (m == -INFINITY ? -INFINITY : kShift + kSlack);
-          if (__any_sync(0xffffffffu, grow)) {
+          const float most = m == -INFINITY ? -INFINITY : kShift + kSlack;
+          if (pair_any(warp & 3, top > most)) {
+            sm.seat[tid] = top;
+            pair_any(warp & 3, false);
+            top = fmaxf(top, sm.seat[tid ^ kWideRows]);
             float f = 1.f;
-            if (grow) {
+            if (top > most) {
               const float now = top + at;
               f = ex2(m - now);
               m = now;
@@ -328,47 +358,45 @@ __global__ void __launch_bounds__(kWideThreads, 2) attend_wide_kernel(const Atte
               __syncwarp();
               tc_after();
 #pragma unroll 1
-              for (int c = 0; c < D; c += 32) {
-                uint32_t o[32];
+              for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 16) {
+                uint32_t o[16];
                 tmem_load(mine + kTmemOut + c, o);
                 tmem_wait_load(o);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
                 tmem_store(mine + kTmemOut + c, o);
               }
             }
             pass();
           }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          l += sum[0] + sum[1];
           tmem_store(sc, p);
           tmem_wait_store();
         } else if (warp_hi > 0) {                             // ... and the products get zeros
-          const uint32_t z[32] = {};
-          tmem_store(mine + b * 64, z);
+          const uint32_t z[16] = {};
+          tmem_store(sc, z);
           tmem_wait_store();
         }
         tc_before();
         bar_arrive(&sm.p_full[b]);
       }
-    } else if (warp < 8) {
-      // ---- keys and values into shared memory
-      const int ft = tid - kSoftThreads;
+    } else if (warp < 16) {
+      // ---- keys (four warps) and values (four) into shared memory
+      const bool is_k = warp < 12;
+      const int ft = tid & (kFillThreads - 1);
       const int c = ft % S::kLanes, key = ft / S::kLanes;     // the thread's piece of its keys
       const int* table = a.block_table + (long long)seq * a.max_blocks;
       const int unit_cols = kUnit / a.block_size, unit_rest = kUnit - unit_cols * a.block_size;
       const long long key0 = u0 * kUnit + key;
+      const uint8_t* pages = static_cast<const uint8_t*>(is_k ? a.k_pages : a.v_pages) + c * 16;
+      const uint8_t* scales = static_cast<const uint8_t*>(is_k ? a.k_block_scales : a.v_block_scales) + c * 2;
+      const long long page = (long long)a.Hkv * a.block_size, head = (long long)h * a.block_size;
       Walk walk[S::kChunks];
       int blk[S::kChunks], next = 0;                          // pages of unit `next`
       struct Codes {
-        uint4 k[S::kChunks], v[S::kChunks];
-        uint32_t ks[S::kChunks], vs[S::kChunks];
-        bool live[S::kChunks];
+        uint4 x[S::kChunks];
+        uint32_t s[S::kChunks];                               // the scales; above them whether the key exists
       } codes[S::kAhead];
-      const uint8_t* kp = static_cast<const uint8_t*>(a.k_pages) + c * 16;
-      const uint8_t* vp = static_cast<const uint8_t*>(a.v_pages) + c * 16;
-      const uint8_t* ksp = static_cast<const uint8_t*>(a.k_block_scales) + c * 2;
-      const uint8_t* vsp = static_cast<const uint8_t*>(a.v_block_scales) + c * 2;
-      const long long page = (long long)a.Hkv * a.block_size, head = (long long)h * a.block_size;
       auto look = [&]() {
 #pragma unroll
         for (int i = 0; i < S::kChunks; ++i)
@@ -378,15 +406,12 @@ __global__ void __launch_bounds__(kWideThreads, 2) attend_wide_kernel(const Atte
       auto fetch = [&](Codes& x) {
 #pragma unroll
         for (int i = 0; i < S::kChunks; ++i) {
-          x.live[i] = (unsigned)blk[i] < (unsigned)a.num_blocks;
-          x.k[i] = x.v[i] = make_uint4(0, 0, 0, 0);
-          x.ks[i] = x.vs[i] = 0;
-          if (x.live[i]) {
-            const long long row = blk[i] * page + (head + walk[i].off);
-            x.k[i] = ld_stream(kp + row * S::kRow);
-            x.v[i] = ld_stream(vp + row * S::kRow);
-            x.ks[i] = __ldg(reinterpret_cast<const unsigned short*>(ksp + row * S::kScaleRow));
-            x.vs[i] = __ldg(reinterpret_cast<const unsigned short*>(vsp + row * S::kScaleRow));
+          x.x[i] = make_uint4(0, 0, 0, 0);
+          x.s[i] = 0;
+          if ((unsigned)blk[i] < (unsigned)a.num_blocks) {
+            const long long at = blk[i] * page + (head + walk[i].off);
+            x.x[i] = ld_stream(pages + at * S::kRow);
+            x.s[i] = __ldg(reinterpret_cast<const unsigned short*>(scales + at * S::kScaleRow)) | 0x10000u;
           }
           walk[i].advance(unit_cols, unit_rest, a.block_size);
         }
@@ -398,53 +423,54 @@ __global__ void __launch_bounds__(kWideThreads, 2) attend_wide_kernel(const Atte
       look();
 #pragma unroll
       for (int j = 0; j < S::kAhead; ++j) fetch(codes[j]);
+      unsigned long long* const free_bar = is_k ? sm.s_full : sm.pv_done;
+      unsigned long long* const full_bar = is_k ? sm.k_full : sm.v_full;
+      uint8_t* const tiles = is_k ? sm.k[0] : sm.v[0];
       for (int step0 = 0; step0 < steps; step0 += S::kAhead) {
 #pragma unroll
         for (int j = 0; j < S::kAhead; ++j) {
           const int step = step0 + j;
           if (step >= steps) break;
           const int n = base + step, b = n & 1;
-          const uint32_t before = ((n >> 1) - 1) & 1;         // the buffer's previous use
-          if (n >= 2) bar_wait(&sm.s_full[b], before, failed);
-#pragma unroll
-          for (int i = 0; i < S::kChunks; ++i)
-            convert(sm.k[b], kUnit * 128, key + i * S::kStep, c, codes[j].k[i], codes[j].ks[i]);
-          fence_async();
-          bar_arrive(&sm.k_full[b]);
-          if (n >= 2) bar_wait(&sm.pv_done[b], before, failed);
+          if (n >= 2) bar_wait(free_bar + b, ((n >> 1) - 1) & 1, failed);   // the buffer's previous use
 #pragma unroll
           for (int i = 0; i < S::kChunks; ++i) {
             const int r = key + i * S::kStep;
-            convert(sm.v[b], kUnit * 128, r, c, codes[j].v[i], codes[j].vs[i]);
-            // (only now has the softmax of the buffer's previous unit read them)
-            if (c == 0) {
-              sm.live[b][r] = codes[j].live[i];
-              if (!codes[j].live[i]) {
-                sm.dead[b] = n;
+            convert(tiles + b * S::kTile, kUnit * 128, r, c, codes[j].x[i], codes[j].s[i] & 0xffffu);
+            if (is_k && c == 0) {
+              const bool live = codes[j].s[i] >> 16;
+              sm.live[n & 3][r] = live;
+              if (!live) {
+                sm.dead[n & 3] = n;
                 // a key that exists but whose page does not is hidden
                 if (key0 + (long long)step * kUnit + i * S::kStep < s.len) set_err(a.err, PSPEC_DEVERR_BLOCK_RANGE);
               }
             }
           }
           fence_async();
-          bar_arrive(&sm.v_full[b]);
+          bar_arrive(full_bar + b);
           fetch(codes[j]);
         }
       }
-    } else if (lane == 0 && steps > 0) {
-      // ---- products
+    } else if (steps > 0) {
+      // ---- products, by one lane; the warp stays together
+      const bool lead = elected();
       const uint64_t qd = tile_desc(smem_addr(sm.q), 16), kd = tile_desc(smem_addr(sm.k[0]), 16),
                      vd = tile_desc(smem_addr(sm.v[0]), kUnit * 128);
       auto scores = [&](int n) {
         const int b = n & 1;
         const uint64_t kb = kd + b * (S::kTile >> 4);
         bar_wait(&sm.k_full[b], (n >> 1) & 1, failed);
+        __syncwarp();
         tc_after();
+        if (lead) {
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          product(tmem + b * 64, qd + ((k >> 2) * (kWideRows * 128) + (k & 3) * 32 >> 4), kb + ((k >> 2) * (kUnit * 128) + (k & 3) * 32 >> 4),
-                  product_kind(kUnit, false), k > 0);
-        tc_commit(&sm.s_full[b]);
+          for (int k = 0; k < D / 16; ++k)
+            product(tmem + b * 64, qd + ((k >> 2) * (kWideRows * 128) + (k & 3) * 32 >> 4), kb + ((k >> 2) * (kUnit * 128) + (k & 3) * 32 >> 4),
+                    product_kind(kUnit, false), k > 0);
+          tc_commit(&sm.s_full[b]);
+        }
+        __syncwarp();
       };
       scores(base);
       if (steps > 1) scores(base + 1);
@@ -453,12 +479,16 @@ __global__ void __launch_bounds__(kWideThreads, 2) attend_wide_kernel(const Atte
         const uint32_t parity = (n >> 1) & 1;
         bar_wait(&sm.v_full[b], parity, failed);
         bar_wait(&sm.p_full[b], parity, failed);
+        __syncwarp();
         tc_after();
+        if (lead) {
 #pragma unroll
-        for (int k = 0; k < kUnit / 16; ++k)
-          product_tmem(tmem + kTmemOut, tmem + b * 64 + k * 8, vd + (b * S::kTile + k * 2048 >> 4),
-                       product_kind(D, true), step > 0 || k > 0);
-        tc_commit(&sm.pv_done[b]);
+          for (int k = 0; k < kUnit / 16; ++k)                // probabilities: 16 columns of each 32
+            product_tmem(tmem + kTmemOut, tmem + b * 64 + (k >> 1) * 32 + (k & 1) * 8, vd + (b * S::kTile + k * 2048 >> 4),
+                         product_kind(D, true), step > 0 || k > 0);
+          tc_commit(&sm.pv_done[b]);
+        }
+        __syncwarp();
         if (step + 2 < steps) {
           bar_wait(&sm.pv_done[b], parity, failed);           // the probabilities have been read
           scores(n + 2);
@@ -472,30 +502,33 @@ __global__ void __launch_bounds__(kWideThreads, 2) attend_wide_kernel(const Atte
     float* part = L.parts + (2LL * cta + (first ? 0 : 1)) * S::kPart;
     first = false;
     const float vscale = a.v_scale ? __ldg(a.v_scale + h) : 1.f;
-    if (warp < 4) {
+    if (warp < 8) {
       if (steps > 0) {
         const int n = base + steps - 1;
         bar_wait(&sm.pv_done[n & 1], (n >> 1) & 1, failed);
         __syncwarp();
         tc_after();
       }
+      sm.seat[tid] = l;
+      pair_any(warp & 3, false);
+      l += sm.seat[tid ^ kWideRows];
 #pragma unroll 1
-      for (int c = 0; c < D; c += 32) {
-        uint32_t o[32];
-        tmem_load(tmem + ((uint32_t)warp << 21) + kTmemOut + c, o);
+      for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 16) {
+        uint32_t o[16];
+        tmem_load(tmem + ((uint32_t)(warp & 3) << 21) + kTmemOut + c, o);
         tmem_wait_load(o);
 #pragma unroll
-        for (int i = 0; i < 32; i += 4) {
+        for (int i = 0; i < 16; i += 4) {
           // (without a key that it sees a row has no output in tensor memory)
           float4 v = make_float4(__uint_as_float(o[i]), __uint_as_float(o[i + 1]), __uint_as_float(o[i + 2]), __uint_as_float(o[i + 3]));
           if (m == -INFINITY && l == 0.f) v = make_float4(0.f, 0.f, 0.f, 0.f);
           if (whole) finish_row<D, uint16_t>(a, rr, c + i, m, l, vscale, v);
-          else *reinterpret_cast<float4*>(part + tid * D + c + i) = v;
+          else *reinterpret_cast<float4*>(part + row * D + c + i) = v;
         }
       }
-      if (!whole) {
-        part[kWideRows * D + tid] = m;
-        part[kWideRows * D + kWideRows + tid] = l;
+      if (!whole && half == 0) {
+        part[kWideRows * D + row] = m;
+        part[kWideRows * D + kWideRows + row] = l;
       }
     }
     base += steps;
@@ -519,7 +552,7 @@ __global__ void __launch_bounds__(kWideThreads, 2) attend_wide_kernel(const Atte
         const int n = (int)(cta_b - cta_a) + 1;
         constexpr int kSeats = kJoinThreads / kWideRows, kHeld = kWideRows * (D / 4) / kJoinThreads;
         const bool joins = tid < kJoinThreads;
-        const int row = tid % kWideRows, place = tid / kWideRows;
+        const int place = tid / kWideRows;
         float M = -INFINITY, sum = 0.f;
         if (joins) {
 #pragma unroll 4
@@ -605,7 +638,8 @@ size_t attend_wide_part_bytes() { return sizeof(float) * 2 * kWideCtas * Wide<12
 
 bool attend_is_wide(const AttendLaunch& L) {
   const long long rows = ((long long)L.a.T * (L.a.Hq / L.a.Hkv) + L.a.B - 1) / L.a.B;
-  return L.a.dtype == PSPEC_BF16 && rows > 32;
+  return L.a.dtype == PSPEC_BF16 && rows > 32 &&
+         (long long)L.a.B * L.a.Hkv * ((rows + kWideRows - 1) / kWideRows) >= kNumSMs / 2;
 }
 
 cudaError_t launch_attend_wide(const AttendLaunch& L, cudaStream_t stream) {

@@ -279,31 +279,46 @@ def test_attend_long_contexts_split_over_the_gpu(D, rows, keys, Hq, Hkv, dtype):
     run_attend(attend_case(7, rows, keys, Hq, Hkv, D, 16, dtype))
 
 
+def wide_heads(rows, group, D):
+    """As many kv heads as it takes for the rows' tiles to fill half of the GPU, and no fewer."""
+    per_seq = (sum(rows) + 3) * group / len(rows)
+    return -(-80 // (len(rows) * max(1, int(-(-per_seq // 128)))))
+
+
 @pytest.mark.parametrize("D", [64, 128])
-@pytest.mark.parametrize("rows,keys,Hq,Hkv,bs", [
-    ([40], [40], 1, 1, 16), ([33], [64], 1, 1, 16), ([64, 64], [65, 700], 2, 2, 16), ([128], [300], 1, 1, 32),
-    ([129, 1], [129, 2000], 2, 1, 16), ([20, 30, 1, 90], [20, 500, 1, 91], 14, 2, 48), ([70], [5000], 8, 1, 20),
-    ([100, 0, 60], [100, 50, 64], 4, 4, 1), ([300, 200], [301, 4000], 3, 1, 64), ([8] * 30, [37 * i + 8 for i in range(30)], 16, 2, 16),
+@pytest.mark.parametrize("rows,keys,group,bs", [
+    ([40], [40], 1, 16), ([33], [64], 1, 16), ([64, 64], [65, 700], 1, 16), ([128], [300], 1, 32),
+    ([129, 1], [129, 2000], 2, 16), ([20, 30, 1, 90], [20, 500, 1, 91], 7, 48), ([70], [5000], 8, 20),
+    ([100, 0, 60], [100, 50, 64], 1, 1), ([300, 200], [301, 1000], 3, 64), ([8] * 30, [37 * i + 8 for i in range(30)], 8, 16),
 ])
-def test_attend_many_rows(rows, keys, Hq, Hkv, bs, D):
+def test_attend_many_rows(rows, keys, group, bs, D):
     """Rows enough for the wide tiles: parts of a tile, several of them, tiles split over CTAs."""
-    run_attend(attend_case(sum(rows) + D, rows, keys, Hq, Hkv, D, bs, torch.bfloat16))
+    H = wide_heads(rows, group, D)
+    run_attend(attend_case(sum(rows) + D, rows, keys, H * group, H, D, bs, torch.bfloat16))
 
 
 @pytest.mark.parametrize("D", [64, 128])
 def test_attend_many_rows_masks_and_scores(D):
     """Wide tiles with rows that see nothing, scattered positions, rejected rows, missing pages,
-    scores far apart, a negative scale, and keys behind every position that hold anything."""
-    c = attend_case(30 + D, [60, 50, 0, 45], [700, 50, 9, 333], 4, 2, D, 16, torch.bfloat16, qscale=8.0)
+    scores far apart, a negative scale, queries that are not aligned, and keys behind every
+    position that hold anything."""
+    rows = [60, 50, 0, 45]
+    H = wide_heads(rows, 2, D)
+    c = attend_case(30 + D, rows, [700, 50, 9, 333], 2 * H, H, D, 16, torch.bfloat16, qscale=8.0)
     g = np.random.default_rng(3)
     c["pos"][:60] = g.integers(-2, 720, 60)
     c["pos"][60:70] = -1
     run_attend(c)
     run_attend(c, scale=-0.2)
     run_attend(c, row_kind=g.integers(0, 5, len(c["pos"])).astype(np.uint8))
+    T, Hq, _ = c["q"].shape
+    wide = torch.randn((T, Hq * D + 24), device=DEV, generator=gen(1)).to(torch.bfloat16)
+    run_attend(c, q=wide[:, 1:1 + Hq * D].view(T, Hq, D))
     c["table"][0, 3], c["table"][3, 20] = -1, c["cache"].k.shape[0]
     run_attend(c, err=b.PSPEC_DEVERR_BLOCK_RANGE)
-    c = attend_case(31 + D, [50, 40], [500, 90], 4, 2, D, 16, torch.bfloat16)
+    rows = [50, 40]
+    H = wide_heads(rows, 2, D)
+    c = attend_case(31 + D, rows, [500, 90], 2 * H, H, D, 16, torch.bfloat16)
     c["pos"][:50], c["pos"][50:90] = np.arange(50) + 30, np.arange(40)
     want = run_attend(c)
     for w in ("k_block_scales", "v_block_scales"):
