@@ -395,7 +395,8 @@ __global__ void __launch_bounds__(kWideThreads, 2) attend_wide_kernel(const Atte
       int blk[S::kChunks], next = 0;                          // pages of unit `next`
       struct Codes {
         uint4 x[S::kChunks];
-        uint32_t s[S::kChunks];                               // the scales; above them whether the key exists
+        uint32_t s[S::kChunks];
+        uint32_t live;                                        // bit i: the key of piece i exists
       } codes[S::kAhead];
       auto look = [&]() {
 #pragma unroll
@@ -408,10 +409,12 @@ __global__ void __launch_bounds__(kWideThreads, 2) attend_wide_kernel(const Atte
         for (int i = 0; i < S::kChunks; ++i) {
           x.x[i] = make_uint4(0, 0, 0, 0);
           x.s[i] = 0;
+          x.live = i == 0 ? 0 : x.live;
           if ((unsigned)blk[i] < (unsigned)a.num_blocks) {
+            x.live |= 1u << i;
             const long long at = blk[i] * page + (head + walk[i].off);
             x.x[i] = ld_stream(pages + at * S::kRow);
-            x.s[i] = __ldg(reinterpret_cast<const unsigned short*>(scales + at * S::kScaleRow)) | 0x10000u;
+            x.s[i] = __ldg(reinterpret_cast<const unsigned short*>(scales + at * S::kScaleRow));
           }
           walk[i].advance(unit_cols, unit_rest, a.block_size);
         }
@@ -436,9 +439,9 @@ __global__ void __launch_bounds__(kWideThreads, 2) attend_wide_kernel(const Atte
 #pragma unroll
           for (int i = 0; i < S::kChunks; ++i) {
             const int r = key + i * S::kStep;
-            convert(tiles + b * S::kTile, kUnit * 128, r, c, codes[j].x[i], codes[j].s[i] & 0xffffu);
+            convert(tiles + b * S::kTile, kUnit * 128, r, c, codes[j].x[i], codes[j].s[i]);
             if (is_k && c == 0) {
-              const bool live = codes[j].s[i] >> 16;
+              const bool live = codes[j].live >> i & 1;
               sm.live[n & 3][r] = live;
               if (!live) {
                 sm.dead[n & 3] = n;
