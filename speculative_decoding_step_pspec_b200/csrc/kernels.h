@@ -156,6 +156,7 @@ struct FilterLaunch {
   int resident;                   // slices live in shared memory
 };
 cudaError_t launch_filter(const FilterLaunch& L, cudaStream_t stream);
+cudaError_t launch_filter_small(const FilterLaunch& L, cudaStream_t stream);   // V <= kFilterSmallV
 
 // pspec_last_launches of this host thread.
 void record_launches(int launches);

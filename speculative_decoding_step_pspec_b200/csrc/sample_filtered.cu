@@ -20,7 +20,7 @@
 // Masses are fp64 sums of fp64 exponentials: the tokens drawn are compared with an exact draw,
 // and with 10^5 tokens kept every 10^-8 of error in the running mass would change one row in a
 // thousand.  Sums are joined in a fixed order, so results repeat.
-#include "common.cuh"
+#include "filter_common.cuh"
 #include "kernels.h"
 
 namespace pspec {
@@ -39,19 +39,8 @@ constexpr int kBins = 4096;              // of a histogram
 constexpr size_t kSliceBytes = 128 * 1024;   // a slice above this is read from global memory
 constexpr float kLowest = -3.402823466e38f;  // tokens below it (-inf) never have mass
 
-__device__ __forceinline__ unsigned ord_of(float x) {       // order-preserving bits
-  const unsigned b = __float_as_uint(x);
-  return b & 0x80000000u ? ~b : b | 0x80000000u;
-}
-__device__ __forceinline__ float value_of(unsigned o) {
-  return __uint_as_float(o & 0x80000000u ? o & 0x7fffffffu : ~o);
-}
-__device__ __forceinline__ unsigned long long key_of(float x, int id) {
-  return (unsigned long long)ord_of(x) << 32 | (0xffffffffu - (unsigned)id);
-}
 // The key below those of every token with this value, above all smaller ones'.
 __device__ __forceinline__ unsigned long long key_floor(float x) { return (unsigned long long)ord_of(x) << 32; }
-__device__ __forceinline__ float clean(float x) { return x == x ? x + 0.f : -INFINITY; }  // NaN, -0
 
 // The same on stored elements, eight (bf16) or four (fp32) at once; their maximum into `top`.
 __device__ __forceinline__ uint32_t clean_pair(uint32_t w) {
@@ -1267,19 +1256,11 @@ __global__ void __launch_bounds__(kFT, 2) filter_kernel(const FilterLaunch L) {
     for (int i = 0; i < 16; ++i) sm.table[tid][(i + tid) & 15] = e;
   }
   if (tid == 0) sm.turn = 0;
-  float temp = a.temperature ? __ldg(a.temperature + seq) : 1.f;
-  float top_p = a.top_p ? __ldg(a.top_p + seq) : 1.f;
-  float min_p = a.min_p ? __ldg(a.min_p + seq) : 0.f;
-  long long k = a.top_k ? __ldg(a.top_k + seq) : 0;
+  const FilterParams prm = filter_params(a, seq, F.rank == 0 && tid == 0);
+  const float temp = prm.temperature, top_p = prm.top_p, min_p = prm.min_p;
+  const long long k = prm.k;
   const double u = (double)__ldg(a.uniforms + at);
-  int bits = 0;
-  if (!(temp >= 0.f) || temp == INFINITY) { temp = 1.f; bits = PSPEC_DEVERR_PARAM_RANGE; }
-  if (top_p != top_p) { top_p = 1.f; bits = PSPEC_DEVERR_PARAM_RANGE; }
-  if (min_p != min_p) { min_p = 0.f; bits = PSPEC_DEVERR_PARAM_RANGE; }
-  if (F.rank == 0 && tid == 0) set_err(a.err, bits);
-  if (min_p > 1.f || top_p <= 0.f) k = 1;                   // only the first token is left
-  if (top_p <= 0.f) top_p = 1.f;
-  const bool k_on = k > 0 && k < a.V, p_on = top_p < 1.f, m_on = min_p > 0.f && min_p <= 1.f;
+  const bool k_on = prm.k_on, p_on = prm.p_on, m_on = prm.m_on;
   // a list needs no mass of the row, and most min-p sets make one
   const bool small = a.V <= kGather, list_k = k_on && k <= kPick;
   const bool mass_first = temp > 0.f && !small && !list_k && !(m_on && !p_on);
@@ -1566,6 +1547,7 @@ cudaError_t launch_tag(FilterLaunch L, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_filter(const FilterLaunch& L, cudaStream_t stream) {
+  if (L.a.V <= kFilterSmallV) return launch_filter_small(L, stream);
   return L.a.dtype == PSPEC_BF16 ? launch_tag<BF16Tag>(L, stream) : launch_tag<F32Tag>(L, stream);
 }
 

@@ -464,7 +464,7 @@ FILTERS = {
 
 @pytest.mark.parametrize("name", FILTERS)
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
-@pytest.mark.parametrize("V", [1, 2, 31, 256, 2049, 40001])
+@pytest.mark.parametrize("V", [1, 2, 31, 100, 256, 513, 2048, 2049, 40001])
 def test_sample_filtered(V, dtype, name):
     B, K = 3, 2
     kw = {n: [v] * B for n, v in FILTERS[name].items()}
@@ -480,7 +480,7 @@ def test_sample_filtered_large_vocabulary(dtype, name):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
-@pytest.mark.parametrize("B,K,V", [(20, 2, 40001), (36, 1, 2050), (400, 4, 5003), (14, 3, 151936)])
+@pytest.mark.parametrize("B,K,V", [(20, 2, 40001), (301, 7, 20), (36, 1, 2050), (400, 4, 5003), (14, 3, 151936)])
 def test_sample_filtered_many_rows(B, K, V, dtype):
     """Batches past the few rows whose slices live in shared memory, every request its own."""
     g = np.random.default_rng(B + V)
