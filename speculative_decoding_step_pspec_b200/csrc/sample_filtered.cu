@@ -36,6 +36,7 @@ constexpr int kChunk = 256;              // 32 lanes x 8 elements
 constexpr int kMaxCluster = 8;
 constexpr long long kFewRows = 32, kManyCtas = 1536;
 constexpr int kBins = 4096;              // of a histogram
+constexpr int kListV = 65536;            // (1758 rows of 4928 logits, mixed filters: TIMES us, 249 with lists)
 constexpr size_t kSliceBytes = 128 * 1024;   // a slice above this is read from global memory
 constexpr float kLowest = -3.402823466e38f;  // tokens below it (-inf) never have mass
 
@@ -1451,7 +1452,9 @@ __global__ void __launch_bounds__(kFT, 2) filter_kernel(const FilterLaunch L) {
       }
       if (in <= 0) break;
       q.reach = true;
-      if (tries == 0 && n_above + in <= kGather) {          // all that is kept makes a list after all
+      // all that is kept makes a list after all: a short one, or one that sorts sooner than the
+      // row's masses are summed
+      if (tries == 0 && (n_above + in <= kFT || (n_above + in <= kGather && a.V > kListV))) {
         got = call_gather(F, lo, INFINITY, 0);
         if (got <= kGather && call_settle(F, got, q, u)) return;
         break;
