@@ -31,11 +31,11 @@ constexpr int kAttThreads = 32 * kAttWarps;
 constexpr int kStep = 16;                       // keys of one warp step
 static_assert(kUnit == kStep * kAttWarps, "a step of each warp");
 constexpr int kStages = 4;
-constexpr int kAttendMaxCtas = kNumSMs * 5;
+constexpr int kAttendMaxCtas = kNumSMs * 4;
 constexpr float kNoMax = -1e30f;                // taken from the exponents of a row without a key
 // Persistent CTAs that fit an SM by their registers.
 constexpr int attend_ctas_per_sm(int D, bool f32, int NT) {
-  return NT == 1 ? (D == 64 ? 5 : (f32 ? 3 : 4)) : (D == 64 && NT == 2 && !f32 ? 4 : (f32 ? 2 : 3));
+  return NT == 1 ? (D == 64 ? 4 : 3) : (D == 64 && NT == 2 && !f32 ? 4 : (f32 ? 2 : 3));
 }
 
 template <int D, int NT>
