@@ -236,11 +236,13 @@ struct Filter {
   __device__ __forceinline__ float inside(int id) const {
     return id >= 0 && id < V ? load_scalar(row, id) : -INFINITY;
   }
+  // (kClean: without NaN and -0, which comparisons do not need)
+  template <bool kClean = true>
   __device__ __forceinline__ void values(const uint4 (&raw)[kRaw], float (&x)[8]) const {
 #pragma unroll
     for (int i = 0; i < kRaw; ++i) {
       uint4 v = raw[i];
-      if constexpr (!kResident) {                           // in shared memory they are clean
+      if constexpr (!kResident && kClean) {                 // in shared memory they are clean
         float top = 0.f;
         clean_vector(v, top, Tag{});
       }
@@ -264,7 +266,7 @@ struct Filter {
 
   // f(v, x) for the eight elements of each of this lane's vectors, whole warps at a time; rows in
   // global memory are fetched a few vectors ahead.
-  template <typename F>
+  template <bool kClean = true, typename F>
   __device__ __forceinline__ void sweep(F&& f) const {
     const int lo = strip_lo(warp), hi = strip_lo(warp + 1);
     constexpr int kAhead = kResident ? 1 : 4 / kRaw;
@@ -279,7 +281,7 @@ struct Filter {
         if (i > 0 && v >= hi) break;
         float x[8];
         if (v + lane < hi) {
-          values(raw[i], x);
+          values<kClean>(raw[i], x);
         } else {
 #pragma unroll
           for (int j = 0; j < 8; ++j) x[j] = -INFINITY;
@@ -362,7 +364,7 @@ struct Filter {
     const unsigned low = (unsigned)cut;
     double a = 0.0;
     int ties = 0;                                           // of the cut's value, kept
-    sweep([&](int v, const float (&x)[8]) {
+    sweep<false>([&](int v, const float (&x)[8]) {
       const unsigned inv = 0xffffffffu - (unsigned)id_of(v, 0);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -395,7 +397,7 @@ struct Filter {
     if (tid == 0) sm.gathered = 0;
     __syncthreads();
     double a = 0.0;
-    sweep([&](int v, const float (&x)[8]) {
+    sweep<false>([&](int v, const float (&x)[8]) {
       unsigned in = 0;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -426,11 +428,19 @@ struct Filter {
   __device__ double join(double& before) {
     FilterSmem& sm = *smem;
     const int n = sm.count;
-    const uint32_t keys = cluster_map(sm.key, 0);
+    if (rank > 0) {
+      const uint32_t keys = cluster_map(sm.key, 0);
+      for (int i = tid; i < n; i += kFT) {
+        unsigned long long key;
+        asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(key) : "r"(keys + 8 * i) : "memory");
+        sm.key[i] = key;
+      }
+    }
+    __syncthreads();
     double a = 0.0;
+#pragma unroll 4
     for (int i = lane; i < n; i += 32) {
-      unsigned long long key;
-      asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(key) : "r"(keys + 8 * i) : "memory");
+      const unsigned long long key = sm.key[i];
       const int v = ((int)(0xffffffffu - (unsigned)key) + lead - c0 * kChunk) >> 3;
       if (v >= strip_lo(warp) && v < strip_lo(warp + 1)) a += weight(value_of((unsigned)(key >> 32)));
     }
@@ -635,24 +645,14 @@ struct Filter {
     if (tid == 0) sm.sum[0] = Part{0.0, sm.gathered};
     return deliver(exchange(1));
   }
-  // The elements of x named by the bits of `in` into this CTA's keys; whole warps.
+  // The elements of x named by the bits of `in` into this CTA's keys.
   __device__ __forceinline__ void collect(int v, const float (&x)[8], unsigned in) const {
-    FilterSmem& sm = *smem;
-    if (!__any_sync(0xffffffffu, in != 0)) return;
-    const int n = __popc(in);
-    int inc = n;
-#pragma unroll
-    for (int s = 1; s < 32; s <<= 1) {
-      const int o = __shfl_up_sync(0xffffffffu, inc, s);
-      if (lane >= s) inc += o;
-    }
-    int at = 0;
-    if (lane == 31) at = atomicAdd(&sm.gathered, inc);
-    at = __shfl_sync(0xffffffffu, at, 31) + inc - n;
+    if (in == 0) return;
+    int at = atomicAdd(&smem->gathered, __popc(in));
 #pragma unroll
     for (int j = 0; j < 8; ++j)
       if (in >> j & 1) {
-        if (at < kGather) sm.key[at] = key_of(x[j], id_of(v, j));
+        if (at < kGather) smem->key[at] = key_of(x[j] + 0.f, id_of(v, j));
         ++at;
       }
   }
@@ -811,22 +811,23 @@ struct Filter {
   // mass lies within e^(+-half its width) of its count times its middle's weight.  Returns the
   // tokens counted in the new bracket, those above it up to the old one in n_above; 0: the mass
   // stays below P; -1: no answer.
-  __device__ int histogram(float& lo, float& hi, double A, double P, int& n_above) {
+  __device__ int histogram(float& lo_out, float& hi_out, double A, double P, int& n_above) {
     FilterSmem& sm = *smem;
-    const float span = hi - lo, s = (float)kBins / span, cf = (float)(c / 128.0);
+    const float lo = lo_out, hi = hi_out;
+    const float span = hi - lo, s = (float)(kBins - 1) / span, cf = (float)(c / 128.0);
     if (!(span > 0.f) || !(s < 1e30f) || !(s > 0.f)) return -1;
     const uint32_t bins = (uint32_t)__cvta_generic_to_shared(sm.bin);
     __syncthreads();
     for (int i = tid; i < kBins; i += kFT) sm.bin[i] = 0;
     __syncthreads();
-    sweep([&](int, const float (&x)[8]) {
+    sweep<false>([&](int, const float (&x)[8]) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        // the part as the low bits of a float between 2^23 and 2^24
-        const float at = fmaxf(fminf(fmaf(x[j] - lo, s, 8388607.5f), 8388608.f + (float)(kBins - 1)), 8388608.f);
+        // the nearest of the parts' middles, as the low bits of a float above 2^23
+        const float at = fmaf(x[j] - lo, s, 8388608.f);
         asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ge.f32 p, %0, %1;\n\tsetp.lt.and.f32 q, %0, %2, p;\n\t"
                      "@q red.shared.add.u32 [%3], 1;\n\t}" ::"f"(x[j]), "f"(lo), "f"(hi),
-                     "r"(bins + ((__float_as_uint(at) & (kBins - 1)) << 2)) : "memory");
+                     "r"(bins + ((__float_as_uint(at) & (2 * kBins - 1)) << 2)));      // (read behind the cluster barrier)
       }
     });
     cluster_sync();
@@ -842,7 +843,7 @@ struct Filter {
         asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(n) : "r"(cluster_map(&sm.bin[b], r)) : "memory");
         count[i] += n;
       }
-      mass += (double)count[i] * (double)ex2((lo + ((float)b + 0.5f) / s - M) * cf);
+      mass += (double)count[i] * (double)ex2((lo + (float)b / s - M) * cf);
       cum[i] = mass;
     }
     double all;
@@ -871,8 +872,8 @@ struct Filter {
     n_above = block_count(above, 1);
     cluster_sync();                                         // the others have read the parts
     if (sure >= kBins) return 0;
-    if (from > 0) hi = lo + (float)(kBins - from) / s;
-    if (to < kBins) lo = lo + (float)(kBins - to) / s;
+    if (from > 0) hi_out = lo + ((float)(kBins - from) - 0.5f) / s;
+    if (to < kBins) lo_out = lo + ((float)(kBins - to) - 0.5f) / s;
     return in;
   }
 
@@ -1170,25 +1171,38 @@ struct Filter {
 // The rarer or larger steps once in the code each, on a copy of the state: its members stay in
 // the kernel's registers.
 template <typename F>
-__device__ __noinline__ float call_pick(F f, int R, double P) { return f.pick(R, P); }
+__device__ __noinline__ float call_pick(F x, int R, double P) {
+  F f = x;
+  return f.pick(R, P);
+}
 template <typename F>
-__device__ __noinline__ int call_gather(F f, float lo, float hi, unsigned long long cut) { return f.gather(lo, hi, cut); }
+__device__ __noinline__ int call_gather(F x, float lo, float hi, unsigned long long cut) {
+  F f = x;
+  return f.gather(lo, hi, cut);
+}
 template <typename F>
-__device__ __noinline__ bool call_settle(F f, int n, typename F::List q, double u) { return f.settle(n, q, u); }
+__device__ __noinline__ bool call_settle(F x, int n, typename F::List q, double u) {
+  F f = x;
+  return f.settle(n, q, u);
+}
 template <typename F>
-__device__ __noinline__ int call_histogram(F f, float& lo, float& hi, double A, double P, int& n_above) {
+__device__ __noinline__ int call_histogram(F x, float& lo, float& hi, double A, double P, int& n_above) {
+  F f = x;
   return f.histogram(lo, hi, A, P, n_above);
 }
 template <typename F>
-__device__ __noinline__ unsigned long long call_select(F f, unsigned long long old, long long k, double P, bool need_mass) {
+__device__ __noinline__ unsigned long long call_select(F x, unsigned long long old, long long k, double P, bool need_mass) {
+  F f = x;
   return f.select(old, k, P, need_mass);
 }
 template <typename F>
-__device__ __noinline__ double call_masses_gather(F f, float lo, float hi, int& n) {
+__device__ __noinline__ double call_masses_gather(F x, float lo, float hi, int& n) {
+  F f = x;
   return f.far ? f.template masses_gather<2>(lo, hi, n) : f.template masses_gather<1>(lo, hi, n);
 }
 template <typename F>
-__device__ __noinline__ double call_masses(F f, unsigned long long cut, double& before) {
+__device__ __noinline__ double call_masses(F x, unsigned long long cut, double& before) {
+  F f = x;
   if (f.far) return f.template masses<false, 2>(max(cut, key_floor(kLowest)), before);
   return cut == 0 ? f.template masses<true, 1>(0, before) : f.template masses<false, 1>(cut, before);
 }
