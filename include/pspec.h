@@ -490,9 +490,10 @@ typedef enum { PSPEC_CACHE_ROWS = 0, PSPEC_CACHE_E2M1 = 1 } pspec_cache_kind;
  * stands for, for callers that attend to the same chunk in 16 bits.
  * One launch.  Outputs must not overlap inputs (PSPEC_ERR_INVALID_ARG).  Limits: D a multiple
  * of 16, D <= 512, rot even, 0 <= rot <= D (PSPEC_ERR_INVALID_ARG otherwise).  Row strides
- * are in elements and at least H*D; rows, pages and outputs of any element alignment are
- * taken, 16-byte aligned ones (bases, and strides times element size) are read and written
- * fastest.  E2M1 pages, and PSPEC_CACHE_ROWS pages, must be 16-byte aligned.
+ * are in elements and at least H*D (which stays below 2^31); rows and outputs of any element
+ * alignment are taken, 16-byte aligned ones (bases, and strides times element size) are read and
+ * written fastest.  Pages of either kind must be 16-byte aligned.  Angles are meant to stay below
+ * 2^45 in magnitude.
  */
 typedef struct {
   int T;                       /* rows; T = 0 is a no-op */
@@ -550,10 +551,12 @@ PSPEC_API pspec_status pspec_append_kv(const pspec_append_args *args, cudaStream
  * or negative block scale counts as 0); keys past seq_lens are not read.
  * One launch: the keys of all sequences and heads are dealt out evenly over the GPU in runs
  * of 64; the CTA that finishes a row tile's last run joins the tile's partial results, in key
- * order.  Workspace: pspec_attend_workspace_bytes() bytes for any batch, 256-byte aligned,
- * zero-filled once before first use (each call leaves its counters at zero).  Calls that
- * share one workspace must not overlap on the GPU.
+ * order.  Workspace: pspec_attend_workspace_bytes() bytes for any batch, 256-byte aligned, its
+ * first PSPEC_ATTEND_ZERO_BYTES zero-filled once before first use (each call leaves its counters
+ * there at zero).  Calls that share one workspace, captured graphs among them, must not overlap
+ * on the GPU.
  */
+#define PSPEC_ATTEND_ZERO_BYTES 4096
 typedef struct {
   int T;                       /* rows of q */
   int B;                       /* sequences; B = 0 or T = 0 is a no-op */
@@ -603,8 +606,9 @@ PSPEC_API pspec_status pspec_attend(const pspec_attend_args *args, void *workspa
  * unless its border is within about 1e-11 of the uniform.  NaN logits count as -inf; a row of
  * -inf alone gives token 0 with probability 0; if logits are +inf, those tokens share the
  * mass equally.  probs (optional) is the drawn token's share of the kept mass.  Any parameter
- * array may be NULL (temperature 1, filters off).  One launch, a cluster of CTAs per row; no
- * workspace.  V is at most PSPEC_FILTER_MAX_V (PSPEC_ERR_UNSUPPORTED above).
+ * array may be NULL (temperature 1, filters off).  One launch, from a warp to a cluster of CTAs
+ * per row; no workspace.  Outputs must not overlap inputs (PSPEC_ERR_INVALID_ARG).  V is at most
+ * PSPEC_FILTER_MAX_V (PSPEC_ERR_UNSUPPORTED above).
  */
 #define PSPEC_FILTER_MAX_V (1 << 24)
 typedef struct {

@@ -26,6 +26,7 @@ PSPEC_ROW_CTX, PSPEC_ROW_NTP, PSPEC_ROW_MASK, PSPEC_ROW_REJ, PSPEC_ROW_PAD = ran
 PSPEC_PADDING_SLOT_ID = -1
 PSPEC_MAX_K = 31
 PSPEC_FILTER_MAX_V = 1 << 24
+PSPEC_ATTEND_ZERO_BYTES = 4096
 
 EXPORTED = (
     "pspec_verify_workspace_bytes", "pspec_verify_greedy", "pspec_verify_rejection",

@@ -5,6 +5,7 @@ binding; every step of the method runs in libpspec's kernels.
 """
 from __future__ import annotations
 
+from contextlib import nullcontext
 from dataclasses import dataclass
 
 import torch
@@ -255,16 +256,28 @@ def _err(device) -> torch.Tensor:
     return torch.zeros((1,), dtype=torch.int32, device=device)
 
 
+def _on(stream, device):
+    """What a call allocates belongs to the stream that it runs on: zeros are written there before
+    the launch, and memory that the call lets go is not handed out again under it."""
+    if stream is None:
+        return nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = (torch.cuda.ExternalStream(int(stream), device=device) if int(stream)
+                  else torch.cuda.default_stream(device))
+    return torch.cuda.stream(stream)
+
+
 def _append(k, v, positions, slot_mapping, cache, q, inv_freq, interleaved, want_values, out,
             stream, prepare):
     o = dict(out) if out is not None else {}
-    if out is None:
-        if q is not None:
-            o["q"] = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        if want_values:
-            o["k"], o["v"] = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (k, v))
-    if "err" not in o:
-        o["err"] = _err(k.device)
+    with _on(stream, k.device):
+        if out is None:
+            if q is not None:
+                o["q"] = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            if want_values:
+                o["k"], o["v"] = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (k, v))
+        if "err" not in o:
+            o["err"] = _err(k.device)
     c = _b.pspec_append_kv(k=k, v=v, positions=positions, slot_mapping=slot_mapping, k_pages=cache.k,
                            v_pages=cache.v, k_block_scales=cache.k_block_scales,
                            v_block_scales=cache.v_block_scales, k_scale=cache.k_scale,
@@ -292,20 +305,24 @@ def prepare_append_kv(k, v, positions, slot_mapping, cache, *, q=None, inv_freq=
 
 
 def attend_workspace(device="cuda") -> torch.Tensor:
-    """Zero-initialised workspace of ``attend``, for any batch; one per stream."""
-    return torch.zeros(_b.pspec_attend_workspace_bytes(), dtype=torch.uint8, device=device)
+    """A workspace of ``attend``, for any batch; one per stream, and per captured graph that may
+    run beside others."""
+    ws = torch.empty(_b.pspec_attend_workspace_bytes(), dtype=torch.uint8, device=device)
+    ws[:_b.PSPEC_ATTEND_ZERO_BYTES].zero_()
+    return ws
 
 
 def _attend(q, cache, block_table, qsl, positions, seq_lens, scale, row_kind, want_lse, workspace,
             out, stream, prepare):
     o = dict(out) if out is not None else {}
-    if "out" not in o:
-        o["out"] = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    if want_lse and "lse" not in o:
-        o["lse"] = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
-    if "err" not in o:
-        o["err"] = _err(q.device)
-    ws = workspace if workspace is not None else attend_workspace(q.device)
+    with _on(stream, q.device):
+        if "out" not in o:
+            o["out"] = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if want_lse and "lse" not in o:
+            o["lse"] = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+        if "err" not in o:
+            o["err"] = _err(q.device)
+        ws = workspace if workspace is not None else attend_workspace(q.device)
     c = _b.pspec_attend(q=q, k_pages=cache.k, v_pages=cache.v, k_block_scales=cache.k_block_scales,
                         v_block_scales=cache.v_block_scales, k_scale=cache.k_scale,
                         v_scale=cache.v_scale, block_table=block_table, qsl=qsl,
@@ -335,12 +352,13 @@ def prepare_attend(q, cache, block_table, qsl, positions, seq_lens, *, scale=Non
 def _filtered(logits, uniforms, temperature, top_k, top_p, min_p, want_probs, out, stream, prepare):
     o = dict(out) if out is not None else {}
     shape, dev = tuple(logits.shape[:2]), logits.device
-    if "tokens" not in o:
-        o["tokens"] = torch.empty(shape, dtype=torch.int32, device=dev)
-    if want_probs and "probs" not in o:
-        o["probs"] = torch.empty(shape, dtype=torch.float32, device=dev)
-    if "err" not in o:
-        o["err"] = _err(dev)
+    with _on(stream, dev):
+        if "tokens" not in o:
+            o["tokens"] = torch.empty(shape, dtype=torch.int32, device=dev)
+        if want_probs and "probs" not in o:
+            o["probs"] = torch.empty(shape, dtype=torch.float32, device=dev)
+        if "err" not in o:
+            o["err"] = _err(dev)
     c = _b.pspec_sample_filtered(logits=logits, uniforms=uniforms, temperature=temperature,
                                  top_k=top_k, top_p=top_p, min_p=min_p, tokens=o["tokens"],
                                  probs=o.get("probs"), err=o["err"], stream=stream, prepare=prepare)

@@ -53,6 +53,7 @@ pspec_status pspec_append_kv(const pspec_append_args* a, cudaStream_t stream) {
     return PSPEC_ERR_INVALID_ARG;
   if (e2m1) scale_bytes = cache_rows * (a->D / 16);
   if (a->q && (!mul(a->Hq, a->D, &q_row) || !mul(q_row * e, a->T, &q_bytes))) return PSPEC_ERR_INVALID_ARG;
+  if (kv_row > 0x7fffffffLL || q_row > 0x7fffffffLL) return PSPEC_ERR_INVALID_ARG;
   long long tmp;
   if (a->k_stride < kv_row || a->v_stride < kv_row || (a->q && a->q_stride < q_row) ||
       !mul(a->T, a->k_stride, &tmp) || !mul(a->T, a->v_stride, &tmp) || (a->q && !mul(a->T, a->q_stride, &tmp)))
@@ -152,6 +153,15 @@ pspec_status pspec_sample_filtered(const pspec_filter_args* a, cudaStream_t stre
   long long tmp;
   if (!mul((long long)a->B * a->K, a->ld, &tmp)) return PSPEC_ERR_INVALID_ARG;
   if ((long long)a->B * a->K * 16 >= 0x7fffffffLL || a->V > PSPEC_FILTER_MAX_V) return PSPEC_ERR_UNSUPPORTED;
+  const long long rows = (long long)a->B * a->K, e = elem_bytes(a->dtype);
+  const Span outs[] = {{a->tokens, 4 * rows}, {a->probs, 4 * rows}};
+  const Span ins[] = {{a->logits, ((rows - 1) * a->ld + a->V) * e}, {a->uniforms, 4 * rows},
+                      {a->temperature, 4LL * a->B}, {a->top_k, 4LL * a->B}, {a->top_p, 4LL * a->B},
+                      {a->min_p, 4LL * a->B}};
+  if (overlap(outs[0], outs[1])) return PSPEC_ERR_INVALID_ARG;
+  for (const Span& o : outs)
+    for (const Span& s : ins)
+      if (overlap(o, s)) return PSPEC_ERR_INVALID_ARG;
   FilterLaunch L{};
   L.a = *a;
   if (launch_filter(L, stream) != cudaSuccess) return PSPEC_ERR_CUDA;

@@ -598,7 +598,10 @@ cudaError_t launch_d(const AttendLaunch& L, cudaStream_t stream) {
 
 }  // namespace
 
-size_t attend_counter_bytes() { return (sizeof(int) * kAttendMaxCtas + 255) / 256 * 256; }
+size_t attend_counter_bytes() {
+  static_assert(sizeof(int) * kAttendMaxCtas <= PSPEC_ATTEND_ZERO_BYTES, "all counters");
+  return PSPEC_ATTEND_ZERO_BYTES;
+}
 size_t attend_workspace_bytes() {
   const size_t parts = sizeof(float) * 2 * kAttendMaxCtas * kMaxPart, wide = attend_wide_part_bytes();
   return (attend_counter_bytes() + (parts > wide ? parts : wide) + 255) / 256 * 256;

@@ -39,6 +39,7 @@ def append_args(**kw):
     dict(k=FAR + 1), dict(k_pages=FAR + 8), dict(slot_mapping=FAR * 5 + 4), dict(positions=FAR * 4 + 2),
     dict(q_out=FAR), dict(q_out=FAR + 512), dict(k_out=FAR * 2), dict(k_pages=FAR * 8),
     dict(k_block_scales=FAR * 8 + 16), dict(k_stride=1 << 61), dict(err=FAR * 16 + 1),
+    dict(Hq=1 << 27, q_stride=1 << 33), dict(Hkv=1 << 26, k_stride=1 << 32, v_stride=1 << 32),
 ])
 def test_append_refuses(kw):
     assert b.LIB.pspec_append_kv(ctypes.byref(append_args(**kw)), None) == b.PSPEC_ERR_INVALID_ARG
@@ -94,7 +95,8 @@ def filter_args(**kw):
 
 @pytest.mark.parametrize("kw,status", [(k, b.PSPEC_ERR_INVALID_ARG) for k in (
     dict(B=-1), dict(K=0), dict(V=0), dict(ld=99), dict(dtype=9), dict(err=None), dict(logits=None),
-    dict(uniforms=None), dict(tokens=None), dict(logits=FAR + 2), dict(top_k=FAR * 4 + 1), dict(ld=1 << 60))]
+    dict(uniforms=None), dict(tokens=None), dict(logits=FAR + 2), dict(top_k=FAR * 4 + 1), dict(ld=1 << 60),
+    dict(tokens=FAR), dict(probs=FAR * 2 + 8), dict(probs=FAR * 7 + 4), dict(tokens=FAR * 3))]
     + [(dict(V=(1 << 24) + 1, ld=1 << 25), b.PSPEC_ERR_UNSUPPORTED),
        (dict(B=1 << 24, K=16), b.PSPEC_ERR_UNSUPPORTED)])
 def test_sample_filtered_refuses(kw, status):

@@ -288,8 +288,8 @@ def wide_heads(rows, group, D):
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("rows,keys,group,bs", [
     ([40], [40], 1, 16), ([33], [64], 1, 16), ([64, 64], [65, 700], 1, 16), ([128], [300], 1, 32),
-    ([129, 1], [129, 2000], 2, 16), ([20, 30, 1, 90], [20, 500, 1, 91], 7, 48), ([70], [5000], 8, 20),
-    ([100, 0, 60], [100, 50, 64], 1, 1), ([300, 200], [301, 1000], 3, 64), ([8] * 30, [37 * i + 8 for i in range(30)], 8, 16),
+    ([129, 1], [129, 1500], 2, 16), ([20, 30, 1, 90], [20, 300, 1, 91], 7, 48), ([70], [2000], 8, 20),
+    ([100, 0, 60], [100, 50, 64], 1, 1), ([300, 200], [301, 500], 3, 64), ([8] * 30, [13 * i + 8 for i in range(30)], 8, 16),
 ])
 def test_attend_many_rows(rows, keys, group, bs, D):
     """Rows enough for the wide tiles: parts of a tile, several of them, tiles split over CTAs."""
@@ -696,6 +696,53 @@ def test_a_decode_step_in_a_graph_and_on_another_stream():
     assert torch.equal(eager["append"]["q"], captured["append"]["q"])
     for n in start:
         assert torch.equal(getattr(cache, n).view(torch.uint8), want[n].view(torch.uint8))
+
+
+def test_what_a_call_allocates_belongs_to_its_stream():
+    """Calls on a side stream, by object and by handle, with nothing given: their zeros, outputs and
+    temporary workspaces are that stream's, whatever the current stream does meanwhile."""
+    c = attend_case(23, [1] * 12, [900] * 12, 8, 2, 64, 16, torch.bfloat16)
+    x, u = logits(24, 6, 2, 3001, torch.float32), uniforms(25, 6, 2)
+    args = (c["q"], c["cache"], i32(c["table"]), i32(c["qsl"]), i32(c["pos"]), i32(c["lens"]))
+    want, drawn = ps.attend(*args), ps.sample_filtered(x, u, want_probs=True)
+    torch.cuda.synchronize()
+    n = int(c["qsl"][-1])
+    s = torch.cuda.Stream()
+    for stream in (s, s.cuda_stream):
+        for _ in range(10):
+            got = ps.attend(*args, stream=stream)
+            tok = ps.sample_filtered(x, u, want_probs=True, stream=stream)
+            torch.full((ps.pspec_attend_workspace_bytes(),), 255, dtype=torch.uint8, device=DEV)   # over what was let go
+        torch.cuda.synchronize()
+        assert got["err"].item() == 0 and tok["err"].item() == 0
+        assert torch.equal(got["out"][:n], want["out"][:n]) and torch.equal(tok["tokens"], drawn["tokens"])
+
+
+def test_two_graphs_and_two_prepared_calls_side_by_side():
+    """Two captured graphs with workspaces of their own, replayed on two streams at once."""
+    cs = [attend_case(26 + i, [4, 1, 9], [700, 90, 2000], 8, 2, D, 16, torch.bfloat16) for i, D in enumerate((64, 128))]
+    want, graphs = [], []
+    for c in cs:
+        args = (c["q"], c["cache"], i32(c["table"]), i32(c["qsl"]), i32(c["pos"]), i32(c["lens"]))
+        call, o = ps.prepare_attend(*args, want_lse=True)
+        call()
+        torch.cuda.synchronize()
+        want.append({k: v.clone() for k, v in o.items()})
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call()
+        o["out"].fill_(-3)
+        graphs.append((g, o, call))
+    streams = [torch.cuda.Stream() for _ in cs]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for (g, _, _), s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    n = 14
+    for (_, o, _), w in zip(graphs, want):
+        assert torch.equal(o["out"][:n], w["out"][:n]) and torch.equal(o["lse"][:n], w["lse"][:n])
 
 
 def test_two_streams_with_their_own_workspaces():
