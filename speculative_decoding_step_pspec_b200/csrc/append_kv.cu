@@ -202,15 +202,18 @@ __device__ __noinline__ uint32_t exact_codes(const typename Tag::elem* head, int
 // How partners are found.
 enum { kAnyhow, kByLane, kInterleaved };   // the first for any rows; the others for 16-byte aligned
 
+// Threads of a CTA: few rows to one, for a padding row leaves its warp's place empty until all end.
+__host__ __device__ constexpr int block_of(int team) { return team == 32 ? 64 : kThreads; }
+
 template <typename Tag, bool kE2M1, int kMode, int kTeam>
-__global__ void __launch_bounds__(kThreads, 3) append_kernel(const AppendLaunch L) {
+__global__ void __launch_bounds__(block_of(kTeam), kTeam == 32 ? 10 : 3) append_kernel(const AppendLaunch L) {
   using elem = typename Tag::elem;
   constexpr int kRaw = Row<Tag>::kRaw, kAhead = kMode == kAnyhow ? 1 : Row<Tag>::kAhead;
   extern __shared__ __align__(16) float2 s_all[];     // [teams][rot / 2] (cos, sin)
   const pspec_append_args& a = L.a;
   const int tid = threadIdx.x % kTeam, team = threadIdx.x / kTeam;
   const int h = a.rot >> 1;
-  const long long t = (long long)blockIdx.x * (kThreads / kTeam) + team;
+  const long long t = (long long)blockIdx.x * (block_of(kTeam) / kTeam) + team;
   float2* s_cs = s_all + team * h;
   if (t >= a.T) return;                               // (whole teams leave)
 
@@ -248,6 +251,7 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(const AppendLaunch 
       fetch8<Tag>(hd < a.Hkv ? ks + hd * a.D : vs + (hd - a.Hkv) * a.D,
                   kMode != kAnyhow || (hd < a.Hkv ? L.vec_k : L.vec_v), raw);
   };
+  float4 held[4];            // (kByLane) the coefficients of the thread's elements, for all heads
   // x turned, of the head whose part at j0 is src; the largest magnitudes that entered, added.  Every lane
   // of the warp comes here.
   auto turn = [&](const elem* src, bool wanted, const uint4 (&raw)[kRaw], float (&x)[8]) {
@@ -264,10 +268,9 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(const AppendLaunch 
     }
     if (!turns || !wanted) return 0.f;
     if constexpr (kMode == kByLane) {                 // whole threads turn
-      const float4* cs = reinterpret_cast<const float4*>(s_cs + (low ? j0 : j0 - h));
 #pragma unroll
       for (int e = 0; e < 8; e += 2) {
-        const float4 v = cs[e >> 1];
+        const float4 v = held[e >> 1];
         reach = fmaxf(reach, fmaxf(fabsf(x[e]), fabsf(x[e + 1])));
         most = fmaxf(most, fmaxf(fabsf(p[e]), fabsf(p[e + 1])));
         x[e] = fmaf(x[e], v.x, p[e] * v.y);
@@ -315,6 +318,11 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(const AppendLaunch 
   if constexpr (kTeam == 32) __syncwarp();
   else __syncthreads();
 
+  if constexpr (kMode == kByLane) {
+    const float4* cs = reinterpret_cast<const float4*>(s_cs + (low ? j0 : j0 - h));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) held[i] = turns ? cs[i] : make_float4(1.f, 0.f, 1.f, 0.f);
+  }
   elem* qo = static_cast<elem*>(a.q_out) + t * a.Hq * a.D + j0;
   for (int i0 = 0; i0 < total_q; i0 += kAhead * groups) {     // the same for every thread
     if (i0 > 0) fetch_q(i0, raw);
@@ -403,7 +411,7 @@ void launch_rows(const AppendLaunch& L, cudaStream_t stream) {
   // A CTA to a row while there are few, else a warp: rows then wait for nothing but their own
   // loads (15360 rows: TEAM).
   const bool warps = a.T > 8 * kNumSMs && a.D <= 256;
-  const int teams = warps ? kThreads / 32 : 1;
+  const int teams = warps ? block_of(32) / 32 : 1;
   const unsigned grid = (unsigned)(((long long)a.T + teams - 1) / teams);
   const size_t smem = (size_t)teams * (a.rot / 2) * sizeof(float2);
   const bool aligned = (!a.q || (L.vec_q && L.vec_qo)) && L.vec_k && L.vec_v && L.vec_ko && L.vec_vo;
@@ -414,7 +422,7 @@ void launch_rows(const AppendLaunch& L, cudaStream_t stream) {
   else if (aligned && a.interleaved) mode = kInterleaved;
   else if (aligned && (nl & (nl - 1)) == 0 && nl <= 32 && a.rot % 16 == 0) mode = kByLane;
   auto go = [&](auto* one, auto* many) {
-    if (warps) many<<<grid, kThreads, smem, stream>>>(L);
+    if (warps) many<<<grid, block_of(32), smem, stream>>>(L);
     else one<<<grid, kThreads, smem, stream>>>(L);
   };
   auto pick = [&](auto e2m1) {
