@@ -206,7 +206,7 @@ enum { kAnyhow, kByLane, kInterleaved };   // the first for any rows; the others
 __host__ __device__ constexpr int block_of(int team) { return team == 32 ? 64 : kThreads; }
 
 template <typename Tag, bool kE2M1, int kMode, int kTeam>
-__global__ void __launch_bounds__(block_of(kTeam), kTeam == 32 ? 10 : 3) append_kernel(const AppendLaunch L) {
+__global__ void __launch_bounds__(block_of(kTeam), kTeam == 32 ? (sizeof(typename Tag::elem) == 2 ? 13 : 10) : 3) append_kernel(const AppendLaunch L) {
   using elem = typename Tag::elem;
   constexpr int kRaw = Row<Tag>::kRaw, kAhead = kMode == kAnyhow ? 1 : Row<Tag>::kAhead;
   extern __shared__ __align__(16) float2 s_all[];     // [teams][rot / 2] (cos, sin)
