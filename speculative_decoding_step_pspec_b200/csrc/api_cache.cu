@@ -115,7 +115,8 @@ pspec_status pspec_attend(const pspec_attend_args* a, void* workspace, size_t wo
   const long long e = elem_bytes(a->dtype);
   long long q_row, out_bytes, slots, cache_rows, tmp;
   if (!mul(a->Hq, a->D, &q_row) || !mul(q_row * e, a->T, &out_bytes) || !mul(a->num_blocks, a->block_size, &slots) ||
-      !mul(slots, (long long)a->Hkv * a->D, &cache_rows) || a->q_stride < q_row || !mul(a->T, a->q_stride, &tmp))
+      !mul(slots, (long long)a->Hkv * a->D, &cache_rows) || a->q_stride < q_row || !mul(a->T, a->q_stride, &tmp) ||
+      (long long)a->Hkv * a->block_size > 0x7fffffffLL)
     return PSPEC_ERR_INVALID_ARG;
   if (a->T == 0 || a->B == 0) { record_launches(0); return PSPEC_OK; }
   if (!a->q || !a->k_pages || !a->v_pages || !a->k_block_scales || !a->v_block_scales || !a->block_table ||

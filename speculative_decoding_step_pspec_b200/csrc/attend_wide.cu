@@ -46,7 +46,7 @@ struct Wide {
   static constexpr int kChunks = D / 64;        // 16-byte pieces of a key's codes per thread
   static constexpr int kLanes = D / 32;         // threads of a key
   static constexpr int kStep = kFillThreads / kLanes;   // keys of one piece
-  static constexpr int kAhead = D == 64 ? 4 : 2;        // units fetched ahead
+  static constexpr int kAhead = D == 64 ? 2 : 1;        // units fetched ahead
   static constexpr long long kPart = kWideRows * (D + 2);
 };
 
@@ -74,8 +74,8 @@ __device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)
 __device__ __forceinline__ void bar_init(unsigned long long* b, int n) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(b)), "r"(n) : "memory");
 }
-__device__ __forceinline__ void bar_arrive(unsigned long long* b) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(b)) : "memory");
+__device__ __forceinline__ void bar_arrive(uint32_t a) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(a) : "memory");
 }
 __device__ __forceinline__ bool bar_done(uint32_t a, uint32_t parity) {
   uint32_t done;
@@ -90,12 +90,14 @@ __device__ __noinline__ void bar_wait_long(uint32_t a, uint32_t parity, volatile
     if (clock64() - start > kWaitClocks) *failed = 1;
   }
 }
-__device__ __forceinline__ void bar_wait(unsigned long long* b, uint32_t parity, volatile int* failed) {
-  const uint32_t a = smem_addr(b);
+__device__ __forceinline__ void bar_wait(uint32_t a, uint32_t parity, volatile int* failed) {
 #pragma unroll 1
   for (int i = 0; i < 8; ++i)
     if (bar_done(a, parity)) return;
   bar_wait_long(a, parity, failed);
+}
+__device__ __forceinline__ void bar_wait(unsigned long long* b, uint32_t parity, volatile int* failed) {
+  bar_wait(smem_addr(b), parity, failed);
 }
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -160,18 +162,18 @@ __device__ __forceinline__ bool elected() {
 // Byte offset of 16-byte chunk c of row r in a swizzled panel.
 __device__ __forceinline__ uint32_t chunk_at(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
 
-// 32 codes (a key's 16-byte piece `c`) with their two block scales into a tile's row.
-__device__ __forceinline__ void convert(uint8_t* tile, int panel_bytes, int row, int c, const uint4& codes, uint32_t scales) {
+// 32 codes (a key's 16-byte piece) with their two block scales as fp16 into four chunks of a
+// tile's row, the first at shared address `at`: chunk i lies 16 i away but for the swizzle.
+__device__ __forceinline__ void convert(uint32_t at, const uint4& codes, uint32_t scales) {
   const uint32_t two = scales_to_half(scales);
   const uint32_t f[2] = {__byte_perm(two, 0, 0x1010), __byte_perm(two, 0, 0x3232)};
   const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
-  uint8_t* p = tile + (c >> 1) * panel_bytes;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     uint32_t h[4];
     codes_to_half(w[i], h);
-    *reinterpret_cast<uint4*>(p + chunk_at(row, (c & 1) * 4 + i)) =
-        make_uint4(hmul2(h[0], f[i >> 1]), hmul2(h[1], f[i >> 1]), hmul2(h[2], f[i >> 1]), hmul2(h[3], f[i >> 1]));
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at ^ (16u * i)), "r"(hmul2(h[0], f[i >> 1])),
+                 "r"(hmul2(h[1], f[i >> 1])), "r"(hmul2(h[2], f[i >> 1])), "r"(hmul2(h[3], f[i >> 1])) : "memory");
   }
 }
 
@@ -288,10 +290,12 @@ __global__ void __launch_bounds__(kWideThreads, 2) attend_wide_kernel(const Atte
     if (warp < 8) {
       // ---- softmax
       const uint32_t mine = tmem + ((uint32_t)(warp & 3) << 21);   // the warp's 32 lanes
-      const int warp_hi = sm.hi[warp & 3], warp_lo = sm.lo[warp & 3];
+      const int warp_hi = sm.hi[warp & 3] < 0 ? -1 : (int)max(0LL, sm.hi[warp & 3] - u0 * kUnit);
+      const int warp_lo = (int)max(0LL, sm.lo[warp & 3] - u0 * kUnit);
+      const int limit = (int)max(0LL, rr.limit - u0 * kUnit);
       for (int step = 0; step < steps; ++step) {
         const int n = base + step, b = n & 1;
-        const long long k0 = (u0 + step) * kUnit;
+        const int k0 = step * kUnit;                          // (limits are counted from there too)
         const uint32_t sc = mine + b * 64 + half * 32;        // the thread's 32 keys
         bar_wait(&sm.s_full[b], (n >> 1) & 1, failed);
         __syncwarp();
@@ -301,7 +305,7 @@ __global__ void __launch_bounds__(kWideThreads, 2) attend_wide_kernel(const Atte
           const bool masked = k0 + kUnit > warp_lo || sm.dead[n & 3] == n;
           uint32_t seen = 0;
           if (masked) {
-            const int left = (int)max(0LL, min(32LL, rr.limit - k0 - half * 32));
+            const int left = max(0, min(32, limit - k0 - half * 32));
 #pragma unroll
             for (int i = 0; i < 4; ++i) {                     // a byte of 0 or 1 per key: eight to bits
               const unsigned long long x = *reinterpret_cast<const unsigned long long*>(&sm.live[n & 3][half * 32 + 8 * i]);
@@ -378,7 +382,7 @@ __global__ void __launch_bounds__(kWideThreads, 2) attend_wide_kernel(const Atte
           tmem_wait_store();
         }
         tc_before();
-        bar_arrive(&sm.p_full[b]);
+        bar_arrive(smem_addr(&sm.p_full[b]));
       }
     } else if (warp < 16) {
       // ---- keys (four warps) and values (four) into shared memory
@@ -387,10 +391,10 @@ __global__ void __launch_bounds__(kWideThreads, 2) attend_wide_kernel(const Atte
       const int c = ft % S::kLanes, key = ft / S::kLanes;     // the thread's piece of its keys
       const int* table = a.block_table + (long long)seq * a.max_blocks;
       const int unit_cols = kUnit / a.block_size, unit_rest = kUnit - unit_cols * a.block_size;
-      const long long key0 = u0 * kUnit + key;
+      const int left = (int)((long long)s.len - u0 * kUnit) - key;    // keys from the thread's first on
       const uint8_t* pages = static_cast<const uint8_t*>(is_k ? a.k_pages : a.v_pages) + c * 16;
       const uint8_t* scales = static_cast<const uint8_t*>(is_k ? a.k_block_scales : a.v_block_scales) + c * 2;
-      const long long page = (long long)a.Hkv * a.block_size, head = (long long)h * a.block_size;
+      const int page = a.Hkv * a.block_size, head = h * a.block_size;
       Walk walk[S::kChunks];
       int blk[S::kChunks], next = 0;                          // pages of unit `next`
       struct Codes {
@@ -401,18 +405,18 @@ __global__ void __launch_bounds__(kWideThreads, 2) attend_wide_kernel(const Atte
       auto look = [&]() {
 #pragma unroll
         for (int i = 0; i < S::kChunks; ++i)
-          blk[i] = next < steps && key0 + (long long)next * kUnit + i * S::kStep < s.len ? __ldg(table + walk[i].col) : -1;
+          blk[i] = next < steps && next * kUnit + i * S::kStep < left ? __ldg(table + walk[i].col) : -1;
       };
       // codes of the unit whose pages were looked up; the next unit's pages are looked up
       auto fetch = [&](Codes& x) {
+        x.live = 0;
 #pragma unroll
         for (int i = 0; i < S::kChunks; ++i) {
           x.x[i] = make_uint4(0, 0, 0, 0);
           x.s[i] = 0;
-          x.live = i == 0 ? 0 : x.live;
           if ((unsigned)blk[i] < (unsigned)a.num_blocks) {
             x.live |= 1u << i;
-            const long long at = blk[i] * page + (head + walk[i].off);
+            const long long at = (long long)blk[i] * page + (head + walk[i].off);
             x.x[i] = ld_stream(pages + at * S::kRow);
             x.s[i] = __ldg(reinterpret_cast<const unsigned short*>(scales + at * S::kScaleRow));
           }
@@ -422,36 +426,35 @@ __global__ void __launch_bounds__(kWideThreads, 2) attend_wide_kernel(const Atte
         look();
       };
 #pragma unroll
-      for (int i = 0; i < S::kChunks; ++i) walk[i].set(key0 + i * S::kStep, a.block_size);
+      for (int i = 0; i < S::kChunks; ++i) walk[i].set(u0 * kUnit + key + i * S::kStep, a.block_size);
       look();
 #pragma unroll
       for (int j = 0; j < S::kAhead; ++j) fetch(codes[j]);
-      unsigned long long* const free_bar = is_k ? sm.s_full : sm.pv_done;
-      unsigned long long* const full_bar = is_k ? sm.k_full : sm.v_full;
-      uint8_t* const tiles = is_k ? sm.k[0] : sm.v[0];
+      const uint32_t free_bar = smem_addr(is_k ? sm.s_full : sm.pv_done), full_bar = smem_addr(is_k ? sm.k_full : sm.v_full);
+      // the thread's first chunk; its other keys lie whole groups of eight rows further
+      const uint32_t dst = smem_addr(is_k ? sm.k[0] : sm.v[0]) + (c >> 1) * (kUnit * 128) + chunk_at(key, (c & 1) * 4);
       for (int step0 = 0; step0 < steps; step0 += S::kAhead) {
 #pragma unroll
         for (int j = 0; j < S::kAhead; ++j) {
           const int step = step0 + j;
           if (step >= steps) break;
           const int n = base + step, b = n & 1;
-          if (n >= 2) bar_wait(free_bar + b, ((n >> 1) - 1) & 1, failed);   // the buffer's previous use
+          if (n >= 2) bar_wait(free_bar + 8 * b, ((n >> 1) - 1) & 1, failed);   // the buffer's previous use
 #pragma unroll
           for (int i = 0; i < S::kChunks; ++i) {
-            const int r = key + i * S::kStep;
-            convert(tiles + b * S::kTile, kUnit * 128, r, c, codes[j].x[i], codes[j].s[i]);
+            convert(dst + b * S::kTile + i * (S::kStep * 128), codes[j].x[i], codes[j].s[i]);
             if (is_k && c == 0) {
               const bool live = codes[j].live >> i & 1;
-              sm.live[n & 3][r] = live;
+              sm.live[n & 3][key + i * S::kStep] = live;
               if (!live) {
                 sm.dead[n & 3] = n;
                 // a key that exists but whose page does not is hidden
-                if (key0 + (long long)step * kUnit + i * S::kStep < s.len) set_err(a.err, PSPEC_DEVERR_BLOCK_RANGE);
+                if (step * kUnit + i * S::kStep < left) set_err(a.err, PSPEC_DEVERR_BLOCK_RANGE);
               }
             }
           }
           fence_async();
-          bar_arrive(full_bar + b);
+          bar_arrive(full_bar + 8 * b);
           fetch(codes[j]);
         }
       }
@@ -641,7 +644,7 @@ size_t attend_wide_part_bytes() { return sizeof(float) * 2 * kWideCtas * Wide<12
 
 bool attend_is_wide(const AttendLaunch& L) {
   const long long rows = ((long long)L.a.T * (L.a.Hq / L.a.Hkv) + L.a.B - 1) / L.a.B;
-  return L.a.dtype == PSPEC_BF16 && rows > 32 &&
+  return L.a.dtype == PSPEC_BF16 && rows > (L.a.D == 64 ? 32 : 40) &&
          (long long)L.a.B * L.a.Hkv * ((rows + kWideRows - 1) / kWideRows) >= kNumSMs / 2;
 }
 
