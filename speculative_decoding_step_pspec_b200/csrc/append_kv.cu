@@ -13,6 +13,11 @@
 // both ends of the interval that holds the exact value, and where the ends differ (a few blocks
 // in ten thousand) the block is done again in fp64, whose borders mid * s * g (3 + 4 + 24
 // significant bits) are exact, so that ties are seen as ties.
+//
+// Measured: 15360 rows (a quarter of them padding) of 64 query and 2 x 8 key and value heads of 64
+// bf16, to 4 bits with the stored values written out: 70 us, 3.5 TB/s or 53 percent of the measured
+// copy bandwidth.  Bound by instructions: 63 percent of the active issue slots, half of the integer
+// pipe.  A call for 15 rows takes 8 to 9 us, which is what a launch takes.
 #include <type_traits>
 
 #include "common.cuh"
@@ -409,7 +414,7 @@ template <typename Tag>
 void launch_rows(const AppendLaunch& L, cudaStream_t stream) {
   const pspec_append_args& a = L.a;
   // A CTA to a row while there are few, else a warp: rows then wait for nothing but their own
-  // loads (15360 rows: TEAM).
+  // loads (15360 rows: 83 us, by CTAs of four rows 101).
   const bool warps = a.T > 8 * kNumSMs && a.D <= 256;
   const int teams = warps ? block_of(32) / 32 : 1;
   const unsigned grid = (unsigned)(((long long)a.T + teams - 1) / teams);

@@ -18,6 +18,11 @@
 // 16 (or 8) bytes of one key ARE its fragments of 8 (or 4) products, and two keys' nibbles
 // interleaved are the pairs that the product with the values wants.  Dequantised values are
 // exact in fp16: 2 significant bits of the code times 4 of the scale, between 2^-10 and 2688.
+//
+// Measured: one token of each of 64 sequences (540 thousand keys in all, 32 heads on 8, D = 128):
+// 182 us, 3.26 TB/s or half of the measured copy bandwidth; the conversions hold the integer pipe
+// at 56 percent and issue at 60, with three CTAs an SM (four: 188 us, five: 202, both for want of
+// registers).  One token over 100000 keys: 52 us, joining 55 parts of a tile the longer tail of it.
 #include "attend_common.cuh"
 
 namespace pspec {
@@ -583,7 +588,7 @@ cudaError_t launch_nt(AttendLaunch L, cudaStream_t stream) {
 
 // The largest tiles that still give every CTA one: fewer leave each to many CTAs, whose results
 // take longer to join than a code takes to be converted again (8 rows of 64 heads over 4096 keys:
-// TIMES).
+// 23 us in tiles of 8 rows, 43 in tiles of 32).
 template <int D, typename Tag>
 cudaError_t launch_d(const AttendLaunch& L, cudaStream_t stream) {
   const long long rows = ((long long)L.a.T * (L.a.Hq / L.a.Hkv) + L.a.B - 1) / L.a.B;
