@@ -20,9 +20,10 @@
 // exact in fp16: 2 significant bits of the code times 4 of the scale, between 2^-10 and 2688.
 //
 // Measured: one token of each of 64 sequences (540 thousand keys in all, 32 heads on 8, D = 128):
-// 182 us, 3.26 TB/s or half of the measured copy bandwidth; the conversions hold the integer pipe
+// 179 us, 3.31 TB/s or half of the measured copy bandwidth; the conversions hold the integer pipe
 // at 56 percent and issue at 60, with three CTAs an SM (four: 188 us, five: 202, both for want of
-// registers).  One token over 100000 keys: 52 us, joining 55 parts of a tile the longer tail of it.
+// registers).  One token over 100000 keys: 52 us, 33 of them at that rate, the
+// rest starting and joining the 55 parts of a tile.
 #include "attend_common.cuh"
 
 namespace pspec {
@@ -545,15 +546,23 @@ attend_kernel(const AttendLaunch L) {
             sum += f * lc;
           }
           __syncthreads();
+          constexpr int kParts = 16 / kHeld;                // sixteen loads in flight
+          for (int c1 = 0; c1 < nb; c1 += kParts) {
+            float4 x[kParts][kHeld];
 #pragma unroll
-          for (int i = 0; i < kHeld; ++i) {
-            const int at = i * kAttThreads + tid, r = at / (D / 4);
-#pragma unroll 8
-            for (int c = 0; c < nb; ++c) {
-              const float4 x = ld_cg(reinterpret_cast<const float4*>(part_of(cta_a + c0 + c)) + at);
-              const float f = factor[c * kTileRows + r];
-              v[i].x += f * x.x; v[i].y += f * x.y; v[i].z += f * x.z; v[i].w += f * x.w;
-            }
+            for (int c = 0; c < kParts; ++c)
+#pragma unroll
+              for (int i = 0; i < kHeld; ++i)
+                x[c][i] = ld_cg(reinterpret_cast<const float4*>(part_of(cta_a + c0 + min(c1 + c, nb - 1))) + i * kAttThreads + tid);
+#pragma unroll
+            for (int c = 0; c < kParts; ++c)
+#pragma unroll
+              for (int i = 0; i < kHeld; ++i) {
+                const float f = c1 + c < nb ? factor[(c1 + c) * kTileRows + (i * kAttThreads + tid) / (D / 4)] : 0.f;
+                if (f != 0.f) {                             // (a part without a key may hold anything)
+                  v[i].x += f * x[c][i].x; v[i].y += f * x[c][i].y; v[i].z += f * x[c][i].z; v[i].w += f * x[c][i].w;
+                }
+              }
           }
         }
         __syncthreads();

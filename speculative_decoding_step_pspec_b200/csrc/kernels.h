@@ -153,7 +153,7 @@ struct FilterLaunch {
   pspec_filter_args a;
   int cluster;                    // CTAs per row
   int chunks_per_cta;             // of 256 elements
-  int resident;                   // slices live in shared memory
+  int heavy_first;                // rows under top-p alone, the longest ones, start first
 };
 cudaError_t launch_filter(const FilterLaunch& L, cudaStream_t stream);
 cudaError_t launch_filter_small(const FilterLaunch& L, cudaStream_t stream);   // V <= kFilterSmallV
