@@ -21,11 +21,10 @@
 // and with 10^5 tokens kept every 10^-8 of error in the running mass would change one row in a
 // thousand.  Sums are joined in a fixed order, so results repeat.
 //
-// Measured: 448 rows of 151936 fp32 logits at their temperatures: 130 us, 2.1 TB/s or 32 percent of
+// Measured: 448 rows of 151936 fp32 logits at their temperatures: 126 us, 2.2 TB/s or 33 percent of
 // the measured copy bandwidth; 33 instructions a logit, 8 of them fp64, fill 62 percent of the
-// active issue slots.  768 rows of 201088 bf16 logits, each request with its own filters: 390 to 460
-// us by the draw of the filters: top-k alone 243, top-p alone 840 (its long nuclei 1100).  7 rows:
-// 14 to 37 us.
+// active issue slots.  768 rows of 201088 bf16 logits, each request with its own filters: 327 us;
+// top-k alone 243, top-p alone 840 (its long nuclei 1100).  7 rows: 14 to 37 us.
 #include "filter_common.cuh"
 #include "kernels.h"
 #include "plan.h"
@@ -1593,7 +1592,8 @@ cudaError_t launch_tag(FilterLaunch L, cudaStream_t stream) {
   // Few rows: the most CTAs a row, its slices in shared memory (7 rows of 201088 bf16 logits: 21 us
   // against 42 by one CTA a row).  Many: fewer CTAs a row, which meet less, and read it again
   // from L2, where more loads are in flight than a slice in shared memory leaves room for (768
-  // such rows: 460 us by two CTAs, 522 by one, 572 by four, 988 by eight with slices).
+  // such rows, mixed filters: 327 us by two CTAs, 390 by one, 490 by four; 988 by eight with slices,
+  // before the long rows started first).
   const bool few = rows <= kFewRows;
   int G = kMaxCluster;
   while (G > 1 && (chunks < 2 * G || (!few && rows * G > kManyCtas))) G >>= 1;
