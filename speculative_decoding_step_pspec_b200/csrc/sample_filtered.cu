@@ -42,7 +42,7 @@ constexpr int kChunk = 256;              // 32 lanes x 8 elements
 constexpr int kMaxCluster = 8;
 constexpr long long kFewRows = 32, kManyCtas = 1536;
 constexpr int kBins = 4096;              // of a histogram
-constexpr int kListV = 65536;            // (1758 rows of 4928 logits, mixed filters: 219 us, 249 with lists)
+constexpr int kListV = 65536;            // (1758 rows of 4928 logits, mixed filters: 214 us, 249 with lists)
 constexpr size_t kSliceBytes = 128 * 1024;   // a slice above this is read from global memory
 constexpr float kLowest = -3.402823466e38f;  // tokens below it (-inf) never have mass
 
@@ -1320,8 +1320,8 @@ __global__ void __launch_bounds__(kFT, 2) filter_kernel(const FilterLaunch L) {
   const double u = (double)__ldg(a.uniforms + at);
   const bool k_on = prm.k_on, p_on = prm.p_on, m_on = prm.m_on;
   // a list needs no mass of the row, and most min-p sets make one
-  const bool small = a.V <= kGather, list_k = k_on && k <= kPick;
-  const bool mass_first = temp > 0.f && !small && !list_k && !(m_on && !p_on);
+  const bool list_k = k_on && k <= kPick;
+  const bool mass_first = temp > 0.f && !list_k && !(m_on && !p_on);
   F.scale_for(temp);
   F.M = 0.f;
   __syncthreads();
@@ -1474,11 +1474,11 @@ __global__ void __launch_bounds__(kFT, 2) filter_kernel(const FilterLaunch L) {
   q.min_x = min_x;
   q.draw = true;
   bool cut_k = k_on, cut_p = p_on;
-  if (small || list_k) {
-    const float t = small ? kLowest : call_pick(F, (int)k, (double)INFINITY);
+  if (list_k) {
+    const float t = call_pick(F, (int)k, (double)INFINITY);
     const int got = call_gather(F, t, INFINITY, 0);
     if (got <= kGather) {
-      if (k_on) q.k = k;
+      q.k = k;
       if (p_on) q.top_p = (double)top_p;
       call_settle(F, got, q, u);
       return;
@@ -1596,13 +1596,16 @@ cudaError_t launch_tag(FilterLaunch L, cudaStream_t stream) {
   // before the long rows started first).
   const bool few = rows <= kFewRows;
   int G = kMaxCluster;
-  while (G > 1 && (chunks < 2 * G || (!few && rows * G > kManyCtas))) G >>= 1;
+  // (a CTA's part of a row is not so short that meeting takes longer: 248 rows of 2371 tokens, top-p,
+  // 62 us by one CTA, 246 by four; 56 rows of 73585, 139 by four, 277 by eight)
+  while (G > 1 && (chunks < (few ? 16 : 64) * G || (!few && rows * G > kManyCtas))) G >>= 1;
   L.cluster = G;
   L.chunks_per_cta = (chunks + G - 1) / G;
   const size_t slice = (size_t)L.chunks_per_cta * kChunk * sizeof(typename Tag::elem);
   const size_t base = filter_smem_base() + (size_t)(kMaxCluster / G) * kFT * 6;
   if (few && slice <= kSliceBytes) return launch_kind<Tag, true>(L, base + slice, stream);
-  L.heavy_first = L.a.top_p && L.a.B > 1 && rows * G > 2 * kNumSMs;
+  // (every CTA looks the sequences over: not for thousands of them)
+  L.heavy_first = L.a.top_p && L.a.B > 1 && L.a.B <= 4096 && rows * G > 2 * kNumSMs;
   return launch_kind<Tag, false>(L, base, stream);
 }
 
