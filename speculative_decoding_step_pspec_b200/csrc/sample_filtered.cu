@@ -89,7 +89,7 @@ __device__ __forceinline__ float load_generic(const float* p) { return *p; }
 struct Yes { static constexpr bool value = true; };
 struct No { static constexpr bool value = false; };
 
-struct Part {            // what a CTA reports of one part of the bracket
+struct Part {            // what a CTA reports: of itself, or of one part of a bracket
   double mass;
   long long count;
 };
@@ -313,19 +313,6 @@ struct Filter {
     cluster_sync();
     if (tid == 0) sm.turn = turn ^ 1;
     return buf;
-  }
-
-  __device__ double block_sum(double v) {                   // to every thread, fixed order
-    FilterSmem& sm = *smem;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    __syncthreads();
-    if (lane == 0) sm.red[warp] = v;
-    __syncthreads();
-    double s = 0.0;
-#pragma unroll
-    for (int w = 0; w < kFW; ++w) s += sm.red[w];
-    return s;
   }
 
   __device__ int block_count(int v, int slot) {             // alternate `slot` between calls
