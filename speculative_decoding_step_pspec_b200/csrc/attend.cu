@@ -281,6 +281,7 @@ attend_kernel(const AttendLaunch L) {
       }
     }
 
+    bool coarse = false;                        // some row's maximum is beyond kCoarse
     for (int step = 0; step < steps; ++step) {
       issue_next(step + kStages - 1);
       asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1));
@@ -337,11 +338,18 @@ attend_kernel(const AttendLaunch L) {
       // ---- softmax in base 2: exponents less what each row takes; the maximum is looked for only
       // when one of them passes the slack
       const bool masked = alive != 0xffffu || k0 + kStep > lim_lo;
-      auto exponents = [&](float (&y)[NT][4]) {
+      auto exponents = [&](float (&y)[NT][4], bool rounded) {
+        if (rounded) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+          for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) y[n][c] = fmaf(sc[n][c], mult[n][c & 1], -at[n][c & 1]);
+            for (int c = 0; c < 4; ++c) y[n][c] = __fadd_rn(__fmul_rn(sc[n][c], mult[n][c & 1]), -at[n][c & 1]);
+        } else {
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) y[n][c] = fmaf(sc[n][c], mult[n][c & 1], -at[n][c & 1]);
+        }
         if (masked) {
 #pragma unroll
           for (int n = 0; n < NT; ++n)
@@ -353,8 +361,8 @@ attend_kernel(const AttendLaunch L) {
         }
       };
       float y[NT][4];
-      exponents(y);
-      bool grow = false;
+      exponents(y, false);
+      bool grow = coarse;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -365,8 +373,8 @@ attend_kernel(const AttendLaunch L) {
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
             float top = -INFINITY;
-            if (y[n][r] > -INFINITY) top = sc[n][r] * mult[n][r];
-            if (y[n][r + 2] > -INFINITY) top = fmaxf(top, sc[n][r + 2] * mult[n][r]);
+            if (y[n][r] > -INFINITY) top = __fmul_rn(sc[n][r], mult[n][r]);
+            if (y[n][r + 2] > -INFINITY) top = fmaxf(top, __fmul_rn(sc[n][r + 2], mult[n][r]));
 #pragma unroll
             for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
             const float old = m[n][r];
@@ -374,6 +382,7 @@ attend_kernel(const AttendLaunch L) {
             if (m[n][r] > old) {
               const float f = ex2(old - m[n][r]);
               at[n][r] = m[n][r] - kShift;
+              coarse |= fabsf(m[n][r]) >= kCoarse;
               l[n][r] *= f;
 #pragma unroll
               for (int j = 0; j < S::kM; ++j) {
@@ -382,7 +391,8 @@ attend_kernel(const AttendLaunch L) {
               }
             }
           }
-        exponents(y);
+        coarse = __any_sync(0xffffffffu, coarse);
+        exponents(y, coarse);
       }
       uint32_t pb[NT][2], pl[kF32 ? NT : 1][2];
 #pragma unroll

@@ -15,6 +15,10 @@ constexpr int kUnit = 64;                       // keys of one unit of work
 // passes it by more than kSlack: both leave them below 2^15 (fp16 holds 65504) and far above
 // fp16's subnormals, and the outputs are rescaled rarely.
 constexpr float kShift = 7.f, kSlack = 8.f;
+// An exponent x - m + kShift is one fused operation on the score, which does not round the product x;
+// the maximum m is a product rounded.  From 2^24 on the two differ by whole octaves (from 2^27: by
+// more than fp16 holds), so where a row has come so far both are rounded, in a second go over the unit.
+constexpr float kCoarse = 16777216.f;
 
 // Four bytes of two e2m1 codes each, as four fp16 pairs (low nibble first).
 __device__ __forceinline__ void codes_to_half(uint32_t w, uint32_t (&h)[4]) {

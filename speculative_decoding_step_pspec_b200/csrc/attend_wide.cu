@@ -292,6 +292,7 @@ __global__ void __launch_bounds__(kWideThreads, 2) attend_wide_kernel(const Atte
     const int steps = max(0, (int)(min(u1, ((long long)max(lim_hi, 0) + kUnit - 1) / kUnit) - u0));
 
     float m = -INFINITY, at = 0.f, l = 0.f;
+    bool coarse = false;                                      // some row of the warp is beyond kCoarse
     if (warp < 8) {
       // ---- softmax
       const uint32_t mine = tmem + ((uint32_t)(warp & 3) << 21);   // the warp's 32 lanes
@@ -321,7 +322,7 @@ __global__ void __launch_bounds__(kWideThreads, 2) attend_wide_kernel(const Atte
           // probabilities by the maximum so far; where one passes the slack, once more by the new
           uint32_t p[16];
           float sum[2], top;
-          auto pass = [&]() {
+          auto pass = [&](bool rounded) {
             float tops[2] = {-INFINITY, -INFINITY};
             sum[0] = sum[1] = 0.f;
 #pragma unroll
@@ -329,8 +330,13 @@ __global__ void __launch_bounds__(kWideThreads, 2) attend_wide_kernel(const Atte
               uint32_t x[16];
               tmem_load(sc + 16 * part, x);
               tmem_wait_load(x);
+              if (rounded) {
 #pragma unroll
-              for (int c = 0; c < 16; ++c) x[c] = __float_as_uint(fmaf(__uint_as_float(x[c]), mult, -at));
+                for (int c = 0; c < 16; ++c) x[c] = __float_as_uint(__fadd_rn(__fmul_rn(__uint_as_float(x[c]), mult), -at));
+              } else {
+#pragma unroll
+                for (int c = 0; c < 16; ++c) x[c] = __float_as_uint(fmaf(__uint_as_float(x[c]), mult, -at));
+              }
               if (masked) {
                 const uint32_t bits = seen >> (16 * part);
 #pragma unroll
@@ -348,15 +354,33 @@ __global__ void __launch_bounds__(kWideThreads, 2) attend_wide_kernel(const Atte
             }
             top = fmaxf(tops[0], tops[1]);
           };
-          pass();
+          pass(false);
           const float most = m == -INFINITY ? -INFINITY : kShift + kSlack;
-          if (pair_any(warp & 3, top > most)) {
+          if (pair_any(warp & 3, top > most || coarse)) {
             sm.seat[tid] = top;
             pair_any(warp & 3, false);
             top = fmaxf(top, sm.seat[tid ^ kWideRows]);
-            float f = 1.f;
+            float f = 1.f, now = top + at;
+            // (both warps of the pair see the same rows, so they agree)
+            coarse = __any_sync(0xffffffffu, coarse || (top > most && fmaxf(fabsf(now), fabsf(at)) >= kCoarse));
+            if (coarse) {                                     // the products themselves
+              now = -INFINITY;
+#pragma unroll 1
+              for (int part = 0; part < 2; ++part) {
+                uint32_t x[16];
+                tmem_load(sc + 16 * part, x);
+                tmem_wait_load(x);
+#pragma unroll
+                for (int c = 0; c < 16; ++c)
+                  if (!masked || (seen >> (16 * part + c) & 1)) now = fmaxf(now, __fmul_rn(__uint_as_float(x[c]), mult));
+              }
+              pair_any(warp & 3, false);
+              sm.seat[tid] = now;
+              pair_any(warp & 3, false);
+              now = fmaxf(now, sm.seat[tid ^ kWideRows]);
+              top = now - at;
+            }
             if (top > most) {
-              const float now = top + at;
               f = ex2(m - now);
               m = now;
               at = now - kShift;
@@ -376,7 +400,7 @@ __global__ void __launch_bounds__(kWideThreads, 2) attend_wide_kernel(const Atte
                 tmem_store(mine + kTmemOut + c, o);
               }
             }
-            pass();
+            pass(coarse);
           }
           l += sum[0] + sum[1];
           tmem_store(sc, p);

@@ -1,0 +1,103 @@
+"""The ends of what the cache and sampling operators admit, on the GPU against their 64-bit references."""
+import numpy as np
+import pytest
+import torch
+
+from tests import ops_reference as R
+from tests.test_cache_ops_gpu import DEV, attend_case, gen, run_attend, wide_heads
+
+pytestmark = pytest.mark.gpu
+
+
+# --------------------------------------------------------------------------- attend
+def one_signed(c, size, seed):
+    """Positive keys against queries of one sign, of about this size."""
+    for w in "kv":
+        getattr(c["cache"], w).bitwise_and_(0x77).bitwise_or_(0x11)
+    c["q"] = (size * (torch.rand(c["q"].shape, device=DEV, generator=gen(seed)) + 0.5)).to(c["q"].dtype)
+    return c
+
+
+def check_largest_alone(c, out):
+    """Where a row's largest score lies above the next by more than both are rounded (D + 8 roundings
+    of 2^-23 each), and by tens, it has probability 1: the row is its value, with one rounding to the
+    dtype and two of factors in fp32.  The weight itself, 2^7 and up to an octave more, is rounded as
+    every probability is -- to fp16 for bf16 rows (half a step is 2^-11 of it), to two fp16 terms for
+    fp32 rows (2^-22) -- and the sum that divides it is not.  Returns how many (row, head) pairs it were."""
+    dtype, (T, Hq, D) = c["q"].dtype, c["q"].shape
+    kv, vv = (R.cache_values(c["cache"], w) for w in "kv")
+    q, got, lse, sure = R.f64(c["q"]), R.f64(out["out"]), R.f64(out["lse"]), 0
+    step = R.HALF_STEP[dtype] + 2.0 ** -22 + (2.0 ** -11 if dtype == torch.bfloat16 else 2.0 ** -22)
+    for i in range(len(c["lens"])):
+        for t in range(c["qsl"][i], c["qsl"][i + 1]):
+            j = np.arange(c["pos"][t] + 1)
+            if not len(j):
+                continue
+            at = c["table"][i, j // c["bs"]], slice(None), j % c["bs"]
+            k, v = kv[at], vv[at]
+            for h in range(Hq):
+                x = k[:, h // (Hq // kv.shape[1])] @ q[t, h] * float(np.float32(D ** -0.5))
+                order = np.argsort(-x)
+                top = x[order[0]]
+                if len(j) > 1 and top - x[order[1]] <= (D + 8) * 2.0 ** -22 * abs(x[order[1]]) + 40:
+                    continue
+                sure += 1
+                want = v[order[0], h // (Hq // kv.shape[1])]
+                assert np.all(np.abs(got[t, h] - want) <= step * 1.01 * np.abs(want)), (t, h)
+                assert abs(lse[t, h] - top) <= (D + 8) * 2.0 ** -23 * abs(top)
+    return sure
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("size", [1e6, 1e8, 1e9, 1e13, 1e20, 1e28])
+@pytest.mark.parametrize("D", [64, 128])
+def test_attend_scores_without_a_fraction(D, size, dtype, sign):
+    """Scores so large that fp32 holds no fraction of them, later no octave."""
+    for rows, keys, Hq, Hkv in (([1, 2], [1, 2], 4, 2), ([8], [300], 8, 1), ([130], [200], 8, 4)):
+        c = one_signed(attend_case(int(D + keys[0]), rows, keys, Hq, Hkv, D, 16, dtype), sign * size, D)
+        assert check_largest_alone(c, run_attend(c)) >= (sum(rows) * Hq // 2 if size > 1e6 else 0)
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("size", [1e6, 1e8, 1e9, 1e13, 1e20, 1e28])
+@pytest.mark.parametrize("D", [64, 128])
+def test_attend_many_rows_scores_without_a_fraction(D, size, sign):
+    H = wide_heads([40, 30], 2, D)
+    c = one_signed(attend_case(D, [40, 30], [40, 150], 2 * H, H, D, 16, torch.bfloat16, extra_rows=0), sign * size, D)
+    c["pos"][:3] = [-1, 0, 1]
+    assert check_largest_alone(c, run_attend(c)) >= (60 * H if size > 1e6 else 0)
+
+
+@pytest.mark.parametrize("many", [False, True])
+@pytest.mark.parametrize("D", [64, 128])
+def test_attend_moderate_scores_after_very_negative_ones(D, many):
+    """The first keys' scores lie past 2^28 below zero, the later ones' within some hundreds of it: the
+    running maximum comes back to where fractions count."""
+    rows = [40, 30] if many else [3, 1]
+    H = wide_heads(rows, 2, D) if many else 2
+    c = attend_case(D, rows, [300, 200], 2 * H, H, D, 16, torch.bfloat16, extra_rows=0, qscale=100.0)
+    pages = c["cache"].k
+    pages[..., 0].bitwise_and_(0xF0)                            # element 0 of every key is zero ...
+    for i in range(2):
+        for j in range(150):                                    # ... but of each sequence's first keys
+            pages[c["table"][i, j // 16], :, j % 16, 0].bitwise_or_(6)
+            c["cache"].k_block_scales.view(torch.uint8)[c["table"][i, j // 16], :, j % 16, 0] = 0x7E
+    c["q"][:, :, 0] = -3e6
+    # scores: element 0 gives the far ones, the rest stays within hundreds
+    out = run_attend(c)
+    q = c["q"].clone()
+    q[:, :, 0] = 0
+    kv, vv = (R.cache_values(c["cache"], w) for w in "kv")
+    _, _, _, a, vmax = R.attend(R.f64(q), kv, vv, c["table"], c["qsl"], c["pos"], c["lens"], D ** -0.5, 16)
+    want = np.zeros(q.shape)
+    for i in range(2):
+        for t in range(c["qsl"][i], c["qsl"][i + 1]):
+            j = np.arange(150, c["pos"][t] + 1)
+            at = c["table"][i, j // 16], slice(None), j % 16
+            for h in range(2 * H):
+                x = kv[at][:, h // 2] @ R.f64(q)[t, h] * D ** -0.5
+                p = np.exp(x - x.max())
+                want[t, h] = p @ vv[at][:, h // 2] / p.sum()
+    bound, _ = R.attend_bounds(torch.bfloat16, D, want, a, vmax)
+    assert np.all(np.abs(R.f64(out["out"]) - want) <= bound)
