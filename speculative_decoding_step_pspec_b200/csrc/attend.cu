@@ -38,7 +38,9 @@ constexpr int kStep = 16;                       // keys of one warp step
 static_assert(kUnit == kStep * kAttWarps, "a step of each warp");
 constexpr int kStages = 4;
 constexpr int kAttendMaxCtas = kNumSMs * 4;
-constexpr float kNoMax = -1e30f;                // taken from the exponents of a row without a key
+// Taken from the exponents of a row without a key yet: the lowest value, so that any score above it
+// passes the slack and becomes the row's maximum.
+constexpr float kNoMax = -3.402823466e38f;
 // Persistent CTAs that fit an SM by their registers.
 constexpr int attend_ctas_per_sm(int D, bool f32, int NT) {
   return NT == 1 ? (D == 64 ? 4 : 3) : (D == 64 && NT == 2 && !f32 ? 4 : (f32 ? 2 : 3));

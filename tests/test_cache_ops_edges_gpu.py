@@ -101,3 +101,23 @@ def test_attend_moderate_scores_after_very_negative_ones(D, many):
                 want[t, h] = p @ vv[at][:, h // 2] / p.sum()
     bound, _ = R.attend_bounds(torch.bfloat16, D, want, a, vmax)
     assert np.all(np.abs(R.f64(out["out"]) - want) <= bound)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("size", [1e30, 1e33, 1e36])
+@pytest.mark.parametrize("D", [64, 128])
+def test_attend_rows_with_very_negative_scores_alone(D, size, dtype):
+    """A row whose visible scores all lie far below zero, of one key or of many, is no empty one."""
+    for rows, keys, Hq, Hkv in (([1, 2], [1, 2], 4, 2), ([8], [300], 8, 1), ([130], [200], 8, 4)):
+        c = one_signed(attend_case(int(D + keys[0]), rows, keys, Hq, Hkv, D, 16, dtype), -size, D)
+        assert check_largest_alone(c, run_attend(c)) >= sum(rows) * Hq // 2
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_attend_very_negative_scores_are_the_same_in_wide_tiles(D):
+    """The same row alone (narrow tiles) and in a batch of many rows (wide ones)."""
+    H = wide_heads([64], 1, D)
+    c = one_signed(attend_case(D, [64], [64], H, H, D, 16, torch.bfloat16, extra_rows=0), -1e33, D)
+    wide = run_attend(c)
+    narrow = run_attend(dict(c, q=c["q"][:1].contiguous(), qsl=np.array([0, 1]), pos=c["pos"][:1]))
+    assert torch.equal(narrow["out"][0], wide["out"][0]) and torch.isfinite(narrow["lse"]).all()
