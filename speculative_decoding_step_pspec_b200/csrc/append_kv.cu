@@ -379,7 +379,9 @@ __global__ void __launch_bounds__(block_of(kTeam), kTeam == 32 ? (sizeof(typenam
       unsigned sc = ends & 0xffu;
       const float s = e4m3_value(sc), per = s > 0.f ? 1.f / (s * g) : 0.f;
       uint32_t packed = 0;
-      bool sure = ends == sc * 0x101u && wide <= 1e30f;
+      // (far from 1 a head scale takes the quotients, and a small rotated value its error, out of fp32's
+      // normal range, where the interval no longer holds the exact value)
+      bool sure = ends == sc * 0x101u && wide <= 1e30f && g > 1e-20f && g < 1e20f && (reach == 0.f || reach > 1e-30f);
       const float room = err * per;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {

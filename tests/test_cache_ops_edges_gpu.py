@@ -3,8 +3,9 @@ import numpy as np
 import pytest
 import torch
 
+import speculative_decoding_step_pspec_b200 as ps
 from tests import ops_reference as R
-from tests.test_cache_ops_gpu import DEV, attend_case, gen, run_attend, wide_heads
+from tests.test_cache_ops_gpu import DEV, attend_case, gen, random_cache, run_attend, wide_heads
 
 pytestmark = pytest.mark.gpu
 
@@ -121,3 +122,36 @@ def test_attend_very_negative_scores_are_the_same_in_wide_tiles(D):
     wide = run_attend(c)
     narrow = run_attend(dict(c, q=c["q"][:1].contiguous(), qsl=np.array([0, 1]), pos=c["pos"][:1]))
     assert torch.equal(narrow["out"][0], wide["out"][0]) and torch.isfinite(narrow["lse"]).all()
+
+
+# --------------------------------------------------------------------------- append
+@pytest.mark.parametrize("rot", [0, 64])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("g", [3e38, 1.5e38, 6e37, 2e-36, 1e-37, 1e-38, 1e-39, 1e-42])
+def test_append_at_the_ends_of_the_head_scales(g, dtype, rot):
+    """Any positive and finite head scale: codes and block scales as if computed exactly, for rows
+    of its size, far smaller and (where fp32 holds them) far larger ones."""
+    T, H, D, bs = 64, 2, 64, 16
+    x = torch.randn((T, H, D), generator=gen(1), device=DEV, dtype=torch.float64)
+    x *= g * 2.0 ** torch.linspace(-12, 12, T, device=DEV, dtype=torch.float64)[:, None, None]
+    x = x.clamp(-1.5e38, 1.5e38).to(dtype)                      # (a rotation stays finite in fp32)
+    x[1::2].abs_()                                              # blocks of one sign, and of both
+    cache = random_cache(gen(2), 4, H, bs, D)
+    cache.k_scale = torch.tensor([g, g * 0.75], device=DEV)
+    cache.v_scale = torch.tensor([g * 0.8, g], device=DEV)
+    pos = torch.arange(T, device=DEV, dtype=torch.int32)
+    inv = (10000.0 ** (-torch.arange(0, rot, 2, device=DEV, dtype=torch.float64) / max(rot, 1))).float()
+    r = ps.append_kv(x, x, pos, torch.arange(T, device=DEV), cache, inv_freq=inv if rot else None)
+    torch.cuda.synchronize()
+    assert r["err"].item() == 0
+    v = R.f64(x)
+    for w, y in (("k", R.rotate(v, pos.cpu().numpy(), R.f64(inv), False)), ("v", v)):
+        code, sc = R.quantise(y, R.f64(getattr(cache, w + "_scale")))
+        got_s = getattr(cache, w + "_block_scales").view(torch.uint8).transpose(1, 2).reshape(T, H, -1).cpu().numpy()
+        got_c = R.unpack(getattr(cache, w).transpose(1, 2).reshape(T, H, -1).cpu().numpy())
+        assert np.array_equal(got_s, sc), np.argwhere(got_s != sc)[:5]
+        mag = np.repeat(sc > 0, 16, -1)                         # a block of scale 0 holds zeros of either sign
+        bad = np.where(mag, got_c != code, got_c & 7 != 0)
+        # a rotated value on the sign's border may be a zero of either sign
+        bad &= ~((got_c & 7 == 0) & (code & 7 == 0) & (np.abs(y) <= 1e-15 * np.abs(v).max(-1, keepdims=True)))
+        assert not bad.any(), np.argwhere(bad)[:5]
