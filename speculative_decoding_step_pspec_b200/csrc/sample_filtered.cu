@@ -1446,8 +1446,26 @@ __global__ void __launch_bounds__(kFT, 2) filter_kernel(const FilterLaunch L) {
     const double limit = (double)min_p * F.weight(F.M);
     o = min(o, om);
     o = o - ol > 4 ? o - 4 : ol;
-    while (o < om && F.weight(value_of(o)) < limit) ++o;
-    min_x = value_of(o) + 0.f;
+    // The border lies a few values above o, as a rule.  Near 0, and at high temperatures, values lie closer
+    // than weights are resolved (2.4e-12), and it may be a billion of them away, on either side.
+    auto holds = [&](unsigned at) { return F.weight(value_of(at)) >= limit; };      // true of om
+    unsigned lo = o, hi = om;
+    if (holds(lo)) {
+      hi = lo;
+      lo = ol;
+      if (holds(lo)) hi = lo;
+    } else {
+      for (int i = 0; i < 8 && hi > lo + 1; ++i) {
+        if (holds(lo + 1)) hi = lo + 1;
+        else ++lo;
+      }
+    }
+    while (hi > lo + 1) {                                   // lo does not hold, hi does
+      const unsigned mid = lo + (hi - lo) / 2;
+      if (holds(mid)) hi = mid;
+      else lo = mid;
+    }
+    min_x = value_of(hi) + 0.f;
   }
 
   // ---- what is kept

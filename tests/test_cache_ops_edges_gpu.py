@@ -5,7 +5,8 @@ import torch
 
 import speculative_decoding_step_pspec_b200 as ps
 from tests import ops_reference as R
-from tests.test_cache_ops_gpu import DEV, attend_case, gen, random_cache, run_attend, wide_heads
+from tests.test_cache_ops_gpu import (DEV, attend_case, gen, random_cache, run_attend, run_filtered, uniforms,
+                                      wide_heads)
 
 pytestmark = pytest.mark.gpu
 
@@ -155,3 +156,34 @@ def test_append_at_the_ends_of_the_head_scales(g, dtype, rot):
         # a rotated value on the sign's border may be a zero of either sign
         bad &= ~((got_c & 7 == 0) & (code & 7 == 0) & (np.abs(y) <= 1e-15 * np.abs(v).max(-1, keepdims=True)))
         assert not bad.any(), np.argwhere(bad)[:5]
+
+
+# --------------------------------------------------------------------------- sample
+@pytest.mark.parametrize("rows", [1, 40])
+def test_sample_filtered_min_p_borders_next_to_zero(rows):
+    """The border value M + t ln(min_p) lies within 1e-15 of 0, where fp32 values are far closer to one
+    another than weights are resolved: it is found in a few steps all the same."""
+    cases = [(2.0, 96, "0x1.800048p-17"), (1.0, 96, "0x1.800048p-18"), (0.7, 27, "0x1.2e6676p-20"),
+             (0.7, 3, "0x1.0ccccep-23"), (1.0, 160, "0x1.400064p-17"), (0.9, 985, "0x1.bb4354p-15")]
+    B, V = len(cases) * rows, 3001
+    x = -torch.rand((B, 1, V), generator=gen(1), device=DEV) - 1e-3
+    t, m = [], []
+    for i in range(B):
+        temperature, j, top = cases[i % len(cases)]
+        top = float.fromhex(top)
+        t.append(temperature)
+        m.append(1 - j * 2.0 ** -24)
+        x[i, 0, 10:20] = top * 0.9                              # kept with the largest
+        x[i, 0, 20:30] = -top                                   # not kept
+        x[i, 0, 17] = top
+    u = uniforms(2, B, 1)
+    run_filtered(x, u, t=t, m=m)
+    a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    call, _ = ps.prepare_sample_filtered(x, u, temperature=torch.tensor(t, device=DEV), min_p=torch.tensor(m, device=DEV))
+    call()
+    torch.cuda.synchronize()
+    a.record()
+    call()
+    b.record()
+    torch.cuda.synchronize()
+    assert a.elapsed_time(b) < 5.0                              # ms; tens of microseconds
