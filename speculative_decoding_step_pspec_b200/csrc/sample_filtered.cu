@@ -1573,7 +1573,11 @@ __global__ void __launch_bounds__(kFT, 2) filter_kernel(const FilterLaunch L) {
 template <typename Tag, bool kResident>
 cudaError_t launch_kind(const FilterLaunch& L, size_t smem, cudaStream_t stream) {
   auto* fn = filter_kernel<Tag, kResident>;
-  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  // The limit belongs to the function, not to this call: always the largest that any call takes, so
+  // that no other host thread's launch finds it lowered.
+  constexpr size_t most = filter_smem_base() + (size_t)kMaxCluster * kFT * 6 + (kResident ? kSliceBytes : 0);
+  static_assert(most <= 227 * 1024, "within the SM's");
+  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeClusterDimension;

@@ -1,12 +1,14 @@
 """The ends of what the cache and sampling operators admit, on the GPU against their 64-bit references."""
+import threading
+
 import numpy as np
 import pytest
 import torch
 
 import speculative_decoding_step_pspec_b200 as ps
 from tests import ops_reference as R
-from tests.test_cache_ops_gpu import (DEV, attend_case, gen, random_cache, run_attend, run_filtered, uniforms,
-                                      wide_heads)
+from tests.test_cache_ops_gpu import (DEV, attend_case, gen, logits, random_cache, run_attend, run_filtered,
+                                      uniforms, wide_heads)
 
 pytestmark = pytest.mark.gpu
 
@@ -187,3 +189,35 @@ def test_sample_filtered_min_p_borders_next_to_zero(rows):
     b.record()
     torch.cuda.synchronize()
     assert a.elapsed_time(b) < 5.0                              # ms; tens of microseconds
+
+
+def test_sample_filtered_from_two_threads_with_other_vocabularies():
+    """Calls of several host threads, each on its stream: none lowers the shared memory that
+    another's launch may take."""
+    sizes = [(4, 7, 201088), (1, 2, 2100), (3, 5, 60000), (2, 4, 9001)]
+    work = []
+    for B, K, V in sizes:
+        x, u = logits(V, B, K, V, torch.bfloat16), uniforms(V + 1, B, K)
+        k = torch.full((B,), 20, dtype=torch.int32, device=DEV)
+        work.append((x, u, k, ps.sample_filtered(x, u, top_k=k)["tokens"]))
+    torch.cuda.synchronize()
+    failed, streams = [], [torch.cuda.Stream() for _ in sizes]
+
+    def loop(i):
+        x, u, k, want = work[i]
+        try:
+            call, o = ps.prepare_sample_filtered(x, u, top_k=k)
+            for _ in range(3000):
+                call(streams[i])
+            streams[i].synchronize()
+            if not torch.equal(o["tokens"], want):
+                failed.append((i, "tokens"))
+        except Exception as e:                                  # noqa: BLE001 (reported below)
+            failed.append((i, repr(e)))
+
+    threads = [threading.Thread(target=loop, args=(i,)) for i in range(len(sizes))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
