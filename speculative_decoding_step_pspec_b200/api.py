@@ -267,9 +267,19 @@ def _on(stream, device):
     return torch.cuda.stream(stream)
 
 
+def _settle(device) -> None:
+    """After the allocations of a prepared call: its zeros are written, and what the current stream did
+    in that memory before is done, when it may be called on whichever stream.  (A call prepared
+    inside a capture belongs to the captured graph, and so do its zeros.)"""
+    with torch.cuda.device(device):
+        if not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream().synchronize()
+
+
 def _append(k, v, positions, slot_mapping, cache, q, inv_freq, interleaved, want_values, out,
             stream, prepare):
-    o = dict(out) if out is not None else {}
+    given = out if out is not None else {}
+    o = dict(given)
     with _on(stream, k.device):
         if out is None:
             if q is not None:
@@ -284,6 +294,8 @@ def _append(k, v, positions, slot_mapping, cache, q, inv_freq, interleaved, want
                            v_scale=cache.v_scale, q=q, inv_freq=inv_freq, interleaved=interleaved,
                            q_out=o.get("q"), k_out=o.get("k"), v_out=o.get("v"), err=o["err"],
                            stream=stream, prepare=prepare)
+    if prepare and len(o) > len(given):
+        _settle(k.device)
     return c, o
 
 
@@ -299,7 +311,9 @@ def append_kv(k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor, slot_ma
 
 def prepare_append_kv(k, v, positions, slot_mapping, cache, *, q=None, inv_freq=None,
                       interleaved=False, want_values=False, out=None) -> tuple:
-    """The arguments of ``append_kv`` marshalled once: (call, outputs), call(stream=None)."""
+    """The arguments of ``append_kv`` marshalled once: (call, outputs), call(stream=None) on any stream.
+    Waits for the current stream where it allocates outputs; call and outputs must be kept until
+    what was launched has run."""
     return _append(k, v, positions, slot_mapping, cache, q, inv_freq, interleaved, want_values, out,
                    None, True)
 
@@ -314,7 +328,8 @@ def attend_workspace(device="cuda") -> torch.Tensor:
 
 def _attend(q, cache, block_table, qsl, positions, seq_lens, scale, row_kind, want_lse, workspace,
             out, stream, prepare):
-    o = dict(out) if out is not None else {}
+    given = out if out is not None else {}
+    o = dict(given)
     with _on(stream, q.device):
         if "out" not in o:
             o["out"] = torch.empty(q.shape, dtype=q.dtype, device=q.device)
@@ -329,6 +344,8 @@ def _attend(q, cache, block_table, qsl, positions, seq_lens, scale, row_kind, wa
                         positions=positions, seq_lens=seq_lens, row_kind=row_kind,
                         scale=q.shape[-1] ** -0.5 if scale is None else scale, out=o["out"],
                         lse=o.get("lse"), err=o["err"], workspace=ws, stream=stream, prepare=prepare)
+    if prepare and (len(o) > len(given) or workspace is None):
+        _settle(q.device)
     return c, o
 
 
@@ -344,13 +361,17 @@ def attend(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, qsl: torc
 
 def prepare_attend(q, cache, block_table, qsl, positions, seq_lens, *, scale=None, row_kind=None,
                    want_lse=False, workspace=None, out=None) -> tuple:
-    """The arguments of ``attend`` marshalled once: (call, outputs), call(stream=None)."""
+    """The arguments of ``attend`` marshalled once: (call, outputs), call(stream=None) on any stream.
+    Without a workspace it makes one, the call's own: launches of one call, its captured graphs
+    among them, must not overlap on the GPU.  Waits for the current stream where it allocates outputs
+    or the workspace; call and outputs must be kept until what was launched has run."""
     return _attend(q, cache, block_table, qsl, positions, seq_lens, scale, row_kind, want_lse,
                    workspace, out, None, True)
 
 
 def _filtered(logits, uniforms, temperature, top_k, top_p, min_p, want_probs, out, stream, prepare):
-    o = dict(out) if out is not None else {}
+    given = out if out is not None else {}
+    o = dict(given)
     shape, dev = tuple(logits.shape[:2]), logits.device
     with _on(stream, dev):
         if "tokens" not in o:
@@ -362,6 +383,8 @@ def _filtered(logits, uniforms, temperature, top_k, top_p, min_p, want_probs, ou
     c = _b.pspec_sample_filtered(logits=logits, uniforms=uniforms, temperature=temperature,
                                  top_k=top_k, top_p=top_p, min_p=min_p, tokens=o["tokens"],
                                  probs=o.get("probs"), err=o["err"], stream=stream, prepare=prepare)
+    if prepare and len(o) > len(given):
+        _settle(dev)
     return c, o
 
 
@@ -377,5 +400,7 @@ def sample_filtered(logits: torch.Tensor, uniforms: torch.Tensor, *,
 
 def prepare_sample_filtered(logits, uniforms, *, temperature=None, top_k=None, top_p=None,
                             min_p=None, want_probs=False, out=None) -> tuple:
-    """The arguments of ``sample_filtered`` marshalled once: (call, outputs), call(stream=None)."""
+    """The arguments of ``sample_filtered`` marshalled once: (call, outputs), call(stream=None) on any
+    stream.  Waits for the current stream where it allocates outputs; call and outputs must be kept
+    until what was launched has run."""
     return _filtered(logits, uniforms, temperature, top_k, top_p, min_p, want_probs, out, None, True)

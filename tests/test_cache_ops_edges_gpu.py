@@ -6,9 +6,10 @@ import pytest
 import torch
 
 import speculative_decoding_step_pspec_b200 as ps
+from speculative_decoding_step_pspec_b200 import _binding as b
 from tests import ops_reference as R
-from tests.test_cache_ops_gpu import (DEV, attend_case, gen, logits, random_cache, run_attend, run_filtered,
-                                      uniforms, wide_heads)
+from tests.test_cache_ops_gpu import (DEV, attend_case, gen, i32, logits, random_cache, run_attend,
+                                      run_filtered, uniforms, wide_heads)
 
 pytestmark = pytest.mark.gpu
 
@@ -221,3 +222,53 @@ def test_sample_filtered_from_two_threads_with_other_vocabularies():
     for t in threads:
         t.join()
     assert not failed, failed
+
+
+# --------------------------------------------------------------------------- prepared calls
+def test_prepared_calls_do_not_run_ahead_of_their_zeros():
+    """Prepared behind work that the current stream has queued, and called at once on another stream:
+    counters and error words are zero before the call and not written after it."""
+    c = attend_case(1, [1, 4], [9000, 3000], 8, 2, 64, 16, torch.bfloat16)
+    args = (c["q"], c["cache"], i32(c["table"]), i32(c["qsl"]), i32(c["pos"]), i32(c["lens"]))
+    x, u = logits(2, 3, 2, 5001, torch.float32), uniforms(3, 3, 2)
+    t = torch.tensor([-1.0, 1.0, 1.0], device=DEV)              # sets the error word
+    k = torch.randn((4, 2, 64), device=DEV).to(torch.bfloat16)
+    pos, slots = torch.zeros(4, dtype=torch.int32, device=DEV), torch.tensor([0, -5, 1, 2], device=DEV)
+    want = ps.attend(*args)
+    n = int(c["qsl"][-1])
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for _ in range(5):
+        junk = torch.full((ps.pspec_attend_workspace_bytes(),), 0x5A, dtype=torch.uint8, device=DEV)
+        del junk                                                # what the workspace will be made of
+        torch.cuda._sleep(50_000_000)                           # some tens of milliseconds
+        attend, o = ps.prepare_attend(*args)
+        attend(s)
+        torch.cuda._sleep(50_000_000)
+        draw, d = ps.prepare_sample_filtered(x, u, temperature=t)
+        draw(s)
+        torch.cuda._sleep(50_000_000)
+        append, a = ps.prepare_append_kv(k, k, pos, slots, c["cache"])
+        append(s)
+        torch.cuda.synchronize()
+        assert o["err"].item() == 0 and torch.equal(o["out"][:n], want["out"][:n])
+        assert d["err"].item() == b.PSPEC_DEVERR_PARAM_RANGE and a["err"].item() == b.PSPEC_DEVERR_BLOCK_RANGE
+        want = ps.attend(*args)                                 # (the cache has changed)
+        torch.cuda.synchronize()
+
+
+def test_calls_prepared_inside_a_capture_belong_to_its_graph():
+    c = attend_case(4, [1, 4], [900, 300], 8, 2, 64, 16, torch.bfloat16)
+    args = (c["q"], c["cache"], i32(c["table"]), i32(c["qsl"]), i32(c["pos"]), i32(c["lens"]))
+    want = ps.attend(*args)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call, o = ps.prepare_attend(*args)
+        call()
+    for _ in range(3):
+        o["out"].fill_(-3)
+        graph.replay()
+    torch.cuda.synchronize()
+    n = int(c["qsl"][-1])
+    assert o["err"].item() == 0 and torch.equal(o["out"][:n], want["out"][:n])
