@@ -13,6 +13,26 @@ import torch
 from . import _binding as _b
 
 
+def _on(stream, device):
+    """What a call allocates belongs to the stream that it runs on: zeros are written there before
+    the launch, and memory that the call lets go is not handed out again under it."""
+    if stream is None:
+        return nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = (torch.cuda.ExternalStream(int(stream), device=device) if int(stream)
+                  else torch.cuda.default_stream(device))
+    return torch.cuda.stream(stream)
+
+
+def _settle(device) -> None:
+    """After the allocations of a prepared call: its zeros are written, and what the current stream did
+    in that memory before is done, when it may be called on whichever stream.  (A call prepared
+    inside a capture belongs to the captured graph, and so do its zeros.)"""
+    with torch.cuda.device(device):
+        if not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream().synchronize()
+
+
 class Workspace:
     """Zero-initialised verify workspace for (B, K, V, mode) and the calls' tuning options
     (None: the process-wide defaults).  Reusable across calls on one stream: each call leaves
@@ -56,9 +76,10 @@ def verify_greedy(target_logits: torch.Tensor, draft_tokens: torch.Tensor, *,
     of pspec_options fields for this call alone."""
     Bn, K1, V = target_logits.shape
     K = K1 - 1
-    o = out if out is not None else verify_outputs(Bn, K, target_logits.device, want_lse, False)
-    ws = workspace if workspace is not None else Workspace(Bn, K, V, False, target_logits.device,
-                                                           options)
+    with _on(stream, target_logits.device):
+        o = out if out is not None else verify_outputs(Bn, K, target_logits.device, want_lse, False)
+        ws = workspace if workspace is not None else Workspace(Bn, K, V, False, target_logits.device,
+                                                               options)
     _b.pspec_verify_greedy(target_logits=target_logits, draft_tokens=draft_tokens,
                           out_tokens=o["out_tokens"], accepted_len=o["accepted_len"],
                           bonus=o["bonus"], err=o["err"], workspace=ws.tensor,
@@ -77,10 +98,11 @@ def verify_rejection(target_logits: torch.Tensor, draft_logits: torch.Tensor,
     residual_mass).  options (optional): a dict of pspec_options fields for this call."""
     Bn, K1, V = target_logits.shape
     K = K1 - 1
-    o = out if out is not None else verify_outputs(Bn, K, target_logits.device, diagnostics, True,
-                                                   residual_mass)
-    ws = workspace if workspace is not None else Workspace(Bn, K, V, True, target_logits.device,
-                                                           options)
+    with _on(stream, target_logits.device):
+        o = out if out is not None else verify_outputs(Bn, K, target_logits.device, diagnostics, True,
+                                                       residual_mass)
+        ws = workspace if workspace is not None else Workspace(Bn, K, V, True, target_logits.device,
+                                                               options)
     _b.pspec_verify_rejection(target_logits=target_logits, draft_logits=draft_logits,
                              draft_tokens=draft_tokens, uniforms=uniforms,
                              out_tokens=o["out_tokens"], accepted_len=o["accepted_len"],
@@ -99,14 +121,15 @@ def sample_drafts(logits: torch.Tensor, uniforms: torch.Tensor | None = None, *,
     [B, K], or the argmax when uniforms is None.  Returns draft_tokens, err (+ q_at_draft)."""
     Bn, K, V = logits.shape
     dev = logits.device
-    o = out if out is not None else {
-        "draft_tokens": torch.empty((Bn, K), dtype=torch.int32, device=dev),
-        "err": torch.zeros((1,), dtype=torch.int32, device=dev),
-    }
-    if want_probs and "q_at_draft" not in o:
-        o["q_at_draft"] = torch.empty((Bn, K), dtype=torch.float32, device=dev)
-    ws = workspace if workspace is not None else torch.zeros(
-        max(256, _b.pspec_sample_workspace_bytes(Bn, K, V)), dtype=torch.uint8, device=dev)
+    with _on(stream, dev):
+        o = out if out is not None else {
+            "draft_tokens": torch.empty((Bn, K), dtype=torch.int32, device=dev),
+            "err": torch.zeros((1,), dtype=torch.int32, device=dev),
+        }
+        if want_probs and "q_at_draft" not in o:
+            o["q_at_draft"] = torch.empty((Bn, K), dtype=torch.float32, device=dev)
+        ws = workspace if workspace is not None else torch.zeros(
+            max(256, _b.pspec_sample_workspace_bytes(Bn, K, V)), dtype=torch.uint8, device=dev)
     _b.pspec_sample_drafts(logits=logits, draft_tokens=o["draft_tokens"], err=o["err"],
                            workspace=ws, uniforms=uniforms, q_at_draft=o.get("q_at_draft"),
                            stream=stream)
@@ -135,8 +158,9 @@ def build_draft_batch(*, K: int, block_size: int, mask_id: int, pad_id: int, T_c
     """P-EAGLE draft-batch construction.  Returns the per-row, per-sequence and hidden
     outputs (see ``include/pspec.h``)."""
     Bn = int(qsl_in.numel()) - 1
-    o = out if out is not None else build_outputs(
-        Bn, K, int(verify_hidden.shape[1]), T_cap, verify_hidden.dtype, verify_hidden.device)
+    with _on(stream, verify_hidden.device):
+        o = out if out is not None else build_outputs(
+            Bn, K, int(verify_hidden.shape[1]), T_cap, verify_hidden.dtype, verify_hidden.device)
     _b.pspec_build_draft_batch(K=K, block_size=block_size, mask_id=mask_id, pad_id=pad_id,
                               T_cap=T_cap, qsl_in=qsl_in, verify_tokens=verify_tokens,
                               verify_pos=verify_pos, accepted_len=accepted_len, bonus=bonus,
@@ -163,11 +187,12 @@ def step(target_logits: torch.Tensor, draft_tokens: torch.Tensor, build: dict, *
     Bn, K1, V = target_logits.shape
     K = K1 - 1
     dev = target_logits.device
-    o = out if out is not None else verify_outputs(Bn, K, dev, False, rej, residual_mass)
-    ws = workspace if workspace is not None else Workspace(Bn, K, V, rej, dev, options)
     vh = build["verify_hidden"]
-    bo = build_out if build_out is not None else build_outputs(
-        Bn, K, int(vh.shape[1]), build["T_cap"], vh.dtype, vh.device)
+    with _on(stream, dev):
+        o = out if out is not None else verify_outputs(Bn, K, dev, False, rej, residual_mass)
+        ws = workspace if workspace is not None else Workspace(Bn, K, V, rej, dev, options)
+        bo = build_out if build_out is not None else build_outputs(
+            Bn, K, int(vh.shape[1]), build["T_cap"], vh.dtype, vh.device)
     bargs = dict(K=build["K"], block_size=build["block_size"], mask_id=build["mask_id"],
                  pad_id=build["pad_id"], T_cap=build["T_cap"], qsl_in=build["qsl_in"],
                  verify_tokens=build["verify_tokens"], verify_pos=build["verify_pos"],
@@ -198,7 +223,8 @@ def prepare_step(target_logits: torch.Tensor, draft_tokens: torch.Tensor, build:
                  build_out=None, k_len: torch.Tensor | None = None, options=None) -> tuple:
     """The arguments of ``step`` marshalled once: returns (call, verify outputs, build
     outputs), where ``call(stream=None)`` runs the step on the same tensors with no further
-    Python-side marshalling (the buffers' contents may change between calls)."""
+    Python-side marshalling (the buffers' contents may change between calls).  Waits for the
+    current stream where it allocates."""
     rej = uniforms is not None
     Bn, K1, V = target_logits.shape
     K = K1 - 1
@@ -222,6 +248,8 @@ def prepare_step(target_logits: torch.Tensor, draft_tokens: torch.Tensor, build:
                            bonus=o["bonus"], err=o["err"], workspace=ws.tensor, build=bargs,
                            draft_logits=draft_logits, uniforms=uniforms,
                            residual_mass=o.get("residual_mass"), k_len=k_len, options=options)
+    if out is None or workspace is None or build_out is None:
+        _settle(dev)
     return call, o, bo
 
 
@@ -254,26 +282,6 @@ class KVCache:
 
 def _err(device) -> torch.Tensor:
     return torch.zeros((1,), dtype=torch.int32, device=device)
-
-
-def _on(stream, device):
-    """What a call allocates belongs to the stream that it runs on: zeros are written there before
-    the launch, and memory that the call lets go is not handed out again under it."""
-    if stream is None:
-        return nullcontext()
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = (torch.cuda.ExternalStream(int(stream), device=device) if int(stream)
-                  else torch.cuda.default_stream(device))
-    return torch.cuda.stream(stream)
-
-
-def _settle(device) -> None:
-    """After the allocations of a prepared call: its zeros are written, and what the current stream did
-    in that memory before is done, when it may be called on whichever stream.  (A call prepared
-    inside a capture belongs to the captured graph, and so do its zeros.)"""
-    with torch.cuda.device(device):
-        if not torch.cuda.is_current_stream_capturing():
-            torch.cuda.current_stream().synchronize()
 
 
 def _append(k, v, positions, slot_mapping, cache, q, inv_freq, interleaved, want_values, out,

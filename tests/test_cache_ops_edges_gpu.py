@@ -7,6 +7,7 @@ import torch
 
 import speculative_decoding_step_pspec_b200 as ps
 from speculative_decoding_step_pspec_b200 import _binding as b
+from speculative_decoding_step_pspec_b200 import inputs as I
 from tests import ops_reference as R
 from tests.test_cache_ops_gpu import (DEV, attend_case, gen, i32, logits, random_cache, run_attend,
                                       run_filtered, uniforms, wide_heads)
@@ -272,3 +273,46 @@ def test_calls_prepared_inside_a_capture_belong_to_its_graph():
     torch.cuda.synchronize()
     n = int(c["qsl"][-1])
     assert o["err"].item() == 0 and torch.equal(o["out"][:n], want["out"][:n])
+
+
+@pytest.mark.parametrize("rejection", [False, True])
+def test_steps_on_another_stream_do_not_run_ahead_of_their_zeros(rejection):
+    """The step, its parts and its prepared call behind work that the current stream has queued, on
+    another stream with nothing given: what they allocate is that stream's, or there already."""
+    w = I.scaled(I.C64, B=6, V=4000, H=64, ctx="uniform", ctx_args=(20, 300))
+    inp = I.build_inputs(w, DEV)
+    d = torch.randint(0, w.V, (w.B, w.K), generator=gen(1), device=DEV, dtype=torch.int32)
+    target, draft = logits(2, w.B, w.K + 1, w.V, torch.bfloat16), logits(3, w.B, w.K, w.V, torch.bfloat16)
+    u = uniforms(4, w.B, w.K + 1)
+    uk = u[:, :w.K].contiguous()
+    kw = dict(draft_logits=draft, uniforms=u) if rejection else {}
+
+    def same(got, want):
+        torch.cuda.synchronize()
+        assert got["err"].item() == 0
+        for n in want:
+            assert torch.equal(got[n], want[n]), n
+
+    want_v, want_b = ps.step(target, d, inp, **kw)
+    want_s = ps.sample_drafts(draft, uk)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for _ in range(3):
+        junk = [torch.full((n,), 0x5A, dtype=torch.uint8, device=DEV) for n in (1 << 20, 1 << 16, 512, 512, 512)]
+        del junk
+        torch.cuda._sleep(50_000_000)
+        call, v, bo = ps.api.prepare_step(target, d, inp, **kw)
+        call(s)
+        torch.cuda._sleep(50_000_000)
+        v2, b2 = ps.step(target, d, inp, stream=s, **kw)
+        if rejection:
+            v3 = ps.verify_rejection(target, draft, d, u, stream=s)
+        else:
+            v3 = ps.verify_greedy(target, d, stream=s)
+        s3 = ps.sample_drafts(draft, uk, stream=s.cuda_stream)
+        same(v, want_v)
+        same(bo, want_b)
+        same(v2, want_v)
+        same(b2, want_b)
+        same(v3, want_v)
+        same(s3, want_s)
