@@ -289,11 +289,9 @@ def _append(k, v, positions, slot_mapping, cache, q, inv_freq, interleaved, want
     given = out if out is not None else {}
     o = dict(given)
     with _on(stream, k.device):
-        if out is None:
-            if q is not None:
-                o["q"] = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-            if want_values:
-                o["k"], o["v"] = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (k, v))
+        for n, t in (("q", q), ("k", k if want_values else None), ("v", v if want_values else None)):
+            if t is not None and n not in o:
+                o[n] = torch.empty(t.shape, dtype=t.dtype, device=t.device)
         if "err" not in o:
             o["err"] = _err(k.device)
     c = _b.pspec_append_kv(k=k, v=v, positions=positions, slot_mapping=slot_mapping, k_pages=cache.k,

@@ -144,6 +144,22 @@ def test_append_binding_refuses(kw, error):
         b.pspec_append_kv(**append_kw(**kw))
 
 
+@pytest.mark.parametrize("given", [(), ("err",), ("q",), ("k",), ("err", "v", "q")])
+def test_append_allocates_the_outputs_that_are_not_given(monkeypatch, given):
+    seen = {}
+    monkeypatch.setattr(b, "pspec_append_kv", lambda **kw: seen.update(kw))
+    all_outs = dict(q=rows(H=4), k=rows(), v=rows(), err=torch.ones(1, dtype=torch.int32))
+    out = {n: all_outs[n] for n in given}
+    kw = append_kw()
+    cache = ps.KVCache(kw["k_pages"], kw["v_pages"], kw["k_block_scales"], kw["v_block_scales"])
+    r = ps.append_kv(kw["k"], kw["v"], kw["positions"], kw["slot_mapping"], cache, q=rows(H=4), want_values=True,
+                     out=out or None)
+    assert set(r) == {"q", "k", "v", "err"} and set(out) == set(given)
+    for n in r:
+        arg = seen[n if n == "err" else n + "_out"]
+        assert arg is r[n] and (arg is out[n] if n in given else arg.shape == all_outs[n].shape)
+
+
 def test_append_binding_refuses_pages_of_another_dtype():
     c = ps.KVCache.zeros(4, 2, 4, 32, dtype=torch.bfloat16, device="cpu")
     with pytest.raises(TypeError):
