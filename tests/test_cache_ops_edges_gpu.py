@@ -9,7 +9,7 @@ import speculative_decoding_step_pspec_b200 as ps
 from speculative_decoding_step_pspec_b200 import _binding as b
 from speculative_decoding_step_pspec_b200 import inputs as I
 from tests import ops_reference as R
-from tests.test_cache_ops_gpu import (DEV, attend_case, gen, i32, logits, random_cache, run_attend,
+from tests.test_cache_ops_gpu import (DEV, LAST, attend_case, gen, i32, logits, random_cache, run_attend,
                                       run_filtered, uniforms, wide_heads)
 
 pytestmark = pytest.mark.gpu
@@ -316,3 +316,58 @@ def test_steps_on_another_stream_do_not_run_ahead_of_their_zeros(rejection):
         same(b2, want_b)
         same(v3, want_v)
         same(s3, want_s)
+
+
+def repeated(x, times, dtype, pad, offset):
+    """x [B, K, V] `times` over, in rows padded by `pad` elements and `offset` of them off alignment."""
+    B, K, V = x.shape
+    flat = torch.zeros((times * B * K * (V + pad) + 8,), dtype=dtype, device=DEV)
+    r = flat[offset:offset + times * B * K * (V + pad)].view(times * B, K, V + pad)[..., :V]
+    r.copy_(x.repeat(times, 1, 1))
+    return r
+
+
+STREAMED = [(torch.float32, 0, 0), (torch.float32, 3, 1), (torch.bfloat16, 0, 0), (torch.bfloat16, 5, 3)]
+
+
+@pytest.mark.parametrize("dtype,pad,offset", STREAMED)
+@pytest.mark.parametrize("V,times", [(3000, 4), (30011, 8)])
+def test_sample_filtered_many_rows_infinities_and_nan(V, times, dtype, pad, offset):
+    """Batches past the few rows whose slices lie in shared memory."""
+    x = logits(14, 6, 2, V, torch.float32)
+    x[0] = -float("inf")                                        # no mass: token 0, probability 0
+    x[1, :, 10:] = -float("inf")                                # masked vocabulary
+    x[2, 0, 77] = x[2, 0, 2900] = float("inf")                  # shares of the infinite
+    x[2, 1] = float("nan")
+    x[3, :, ::2] = float("nan")
+    x[4] = -float("inf")
+    x[4, :, 1234] = -1e38
+    x[5] *= 1e37
+    x, B = repeated(x, times, dtype, pad, offset), 6 * times
+    u = uniforms(15, B, 2)
+    for kw in ({}, dict(k=5), dict(p=0.5), dict(t=0.0), dict(m=0.3), dict(k=2500), dict(p=0.99, m=1e-4), dict(k=2000, p=0.9)):
+        r = run_filtered(x, u, **{n: [v] * B for n, v in kw.items()})
+        assert (r["tokens"][::6] == 0).all() and (r["probs"][::6] == 0).all() and (r["tokens"][4::6] == 1234).all()
+
+
+@pytest.mark.parametrize("dtype,pad,offset", STREAMED)
+def test_sample_filtered_many_rows_of_ties(dtype, pad, offset):
+    """Few distinct logits, -0 among them: cuts inside a class of ties larger than one CTA sorts."""
+    V = 30011
+    x = torch.randint(0, 3, (6, 2, V), generator=gen(11), device=DEV).float()
+    x[5, :, ::2] *= -0.0
+    x, B = repeated(x, 4, dtype, pad, offset), 24
+    u = uniforms(12, B, 2)
+    run_filtered(x, u, k=[1, 4000, 15000, 25000, 29000, 0] * 4, p=[1, 1, 1, 1, 1, 0.3] * 4)
+    run_filtered(x, u, p=[0.01, 0.2, 0.5, 0.7, 0.97, 0.9999] * 4)
+    run_filtered(x, u, k=[5000, 6000, 12000, 20000, 25000, 29999] * 4, p=[0.5, 0.9, 0.99, 0.8, 0.3, 0.7] * 4)
+    run_filtered(x, u, p=[0.01, 0.2, 0.5, 0.7, 0.97, 0.9999] * 4, m=[0.1, 0.3, 1.0, 0.14, 0.5, 0.0] * 4)
+    same = repeated(torch.full((3, 2, V), -2.5, device=DEV), 8, dtype, pad, offset)
+    run_filtered(same, u, k=[0, 9000, 0] * 8, p=[1, 1, 0.25] * 8, m=[0, 0, 1.0] * 8)
+
+
+@pytest.mark.parametrize("dtype,pad,offset", STREAMED)
+def test_sample_filtered_many_rows_at_extreme_uniforms(dtype, pad, offset):
+    x = repeated(logits(16, 4, 2, 4000, torch.float32), 6, dtype, pad, offset)
+    edge = torch.tensor([[0.0, LAST]] * 24, device=DEV)
+    run_filtered(x, edge, t=[1, 0.3, 1, 1] * 6, k=[0, 0, 30, 0] * 6, p=[1, 1, 1, 0.9] * 6)
