@@ -202,11 +202,12 @@ struct Filter {
     zero_below = fmaxf((float)(-1020.0 * 128.0 / c), kLowest);
     while ((double)zero_below * c < -1021.0 * 128.0) zero_below = value_of(ord_of(zero_below) + 1);
   }
-  // ... and whether that held; else the factors relative to it.
+  // ... and whether that held; else the factors relative to it.  So hot that even the lowest finite
+  // logit weighs something, -inf (clamped to it outside `far`) has to be told apart.
   __device__ __forceinline__ bool rescale() {
     const double y = (double)M * c;
-    if (fabs(y) <= 900.0 * 128.0) return true;
-    far = !(fabs(y) < 1073741824.0);
+    if (fabs(y) <= 900.0 * 128.0 && (double)kLowest * c <= -1020.0 * 128.0) return true;
+    far = !(fabs(y) < 1073741824.0) || ((double)kLowest - (double)M) * c > -1000.0 * 128.0;
     bias = far ? 0 : 128 * (int)rint(y / 128.0);
     const double Md = (double)M;
     float z = fmaxf((float)(Md - 1000.0 * 128.0 / c), kLowest);

@@ -371,3 +371,20 @@ def test_sample_filtered_many_rows_at_extreme_uniforms(dtype, pad, offset):
     x = repeated(logits(16, 4, 2, 4000, torch.float32), 6, dtype, pad, offset)
     edge = torch.tensor([[0.0, LAST]] * 24, device=DEV)
     run_filtered(x, edge, t=[1, 0.3, 1, 1] * 6, k=[0, 0, 30, 0] * 6, p=[1, 1, 1, 0.9] * 6)
+
+
+@pytest.mark.parametrize("times", [1, 5])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_sample_filtered_so_hot_that_the_lowest_logit_weighs(dtype, times):
+    """Temperatures at which every finite logit has a share: tokens at -inf, and what lies past a row's
+    end, still have none."""
+    t = [1e35, 5e35, 1e36, 1e37, 1e38, 3.4e38, 1e36, 1e36]
+    B, V = len(t) * times, 5003
+    x = logits(23, B, 2, V, torch.float32, sigma=1.0)
+    x[::2] *= 1e38
+    x[:, :, 1::3] = -float("inf")
+    x[6::8] = (x[6::8].clamp(-10, 10) * 1e34) - 3.2e38          # all near the lowest
+    x = x.to(dtype)
+    u = uniforms(24, B, 2)
+    for kw in ({}, dict(k=7), dict(k=2000), dict(p=0.3), dict(p=0.9), dict(m=0.5), dict(p=0.7, m=0.01), dict(k=400, p=0.6)):
+        run_filtered(x, u, t=t * times, **{n: [v] * B for n, v in kw.items()})
