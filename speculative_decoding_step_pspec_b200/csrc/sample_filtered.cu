@@ -868,7 +868,7 @@ struct Filter {
     if (sure >= kBins) return 0;
     if (from > 0) hi_out = lo + ((float)(kBins - from) - 0.5f) / s;
     if (to < kBins) lo_out = lo + ((float)(kBins - to) - 0.5f) / s;
-    return in;
+    return in > 0 ? in : -1;                                // (estimates that are not finite say nothing)
   }
 
   // ------------------------------------------------------------------ exact narrowing

@@ -388,3 +388,18 @@ def test_sample_filtered_so_hot_that_the_lowest_logit_weighs(dtype, times):
     u = uniforms(24, B, 2)
     for kw in ({}, dict(k=7), dict(k=2000), dict(p=0.3), dict(p=0.9), dict(m=0.5), dict(p=0.7, m=0.01), dict(k=400, p=0.6)):
         run_filtered(x, u, t=t * times, **{n: [v] * B for n, v in kw.items()})
+
+
+@pytest.mark.parametrize("times", [1, 3])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V", [1000, 9001])
+def test_sample_filtered_extreme_temperatures(V, dtype, times):
+    """From the smallest that fp32 holds to near its largest: one token's share, and equal shares."""
+    t = [1e-45, 1e-38, 1e-20, 1e-6, 1e-3, 1e3, 1e6, 1e12, 1e30, 3e38]
+    B = len(t) * times
+    x = logits(21, B, 2, V, dtype)
+    u = uniforms(22, B, 2)
+    for kw in ({}, dict(k=7), dict(k=2000), dict(p=0.3), dict(p=0.9), dict(m=0.5), dict(p=0.7, m=0.01), dict(k=400, p=0.6)):
+        for shift in (0.0, 1000.0, -1e6):
+            run_filtered(x + torch.full((), shift, dtype=dtype, device=DEV), u, t=t * times,
+                         **{n: [v] * B for n, v in kw.items()})
