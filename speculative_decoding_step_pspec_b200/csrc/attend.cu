@@ -246,9 +246,9 @@ attend_kernel(const AttendLaunch L) {
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
         // 2^(14 - exponent of the row's largest element), kept within fp32's normal range
         const int ex = (int)(__float_as_uint(top) >> 23) - 127;
-        const int up = top == 0.f || ex == 128 ? 0 : min(100, 14 - ex);
+        const int up = top == 0.f || ex == 128 ? 0 : min(126, 14 - ex);
         const float f = __uint_as_float((unsigned)(127 + up) << 23);
-        const float back = a.scale * kLog2e * ks * __uint_as_float((unsigned)(127 - up) << 23);
+        const float back = score_factor(a.scale, ks, up);
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           mult[n][r] = __shfl_sync(0xffffffffu, back, (2 * t + r) * 4);

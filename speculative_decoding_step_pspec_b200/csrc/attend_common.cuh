@@ -108,6 +108,12 @@ __device__ __forceinline__ RowRef row_of(const pspec_attend_args& a, const Seq& 
   return x;
 }
 
+// The factor of a row's scores in base 2, its queries having been multiplied by 2^up.  The head scale
+// meets that power first: each may lie where its product with another factor would leave fp32.
+__device__ __forceinline__ float score_factor(float scale, float kscale, int up) {
+  return scale * kLog2e * (kscale * __uint_as_float((unsigned)(127 - up) << 23));
+}
+
 __device__ __forceinline__ void load_q2(const uint16_t* p, float& x, float& y) {
   x = __uint_as_float((uint32_t)__ldg(reinterpret_cast<const unsigned short*>(p)) << 16);
   y = __uint_as_float((uint32_t)__ldg(reinterpret_cast<const unsigned short*>(p) + 1) << 16);
@@ -211,8 +217,12 @@ template <int D, typename elem>
 __device__ __forceinline__ void finish_row(const pspec_attend_args& a, const RowRef& rr, int d, float M, float sum,
                                            float vscale, float4 v) {
   if (rr.limit < 0) return;
-  const float f = sum > 0.f ? vscale / sum : (sum == 0.f ? 0.f : sum);
-  store_out(static_cast<elem*>(a.out) + rr.at * D + d, make_float4(v.x * f, v.y * f, v.z * f, v.w * f));
+  float f = sum > 0.f ? vscale / sum : (sum == 0.f ? 0.f : sum), g = 1.f;
+  if (f < 1e-37f && sum > 0.f) {                  // a quotient below fp32's normal range: in two factors
+    f = 1.f / sum;
+    g = vscale;
+  }
+  store_out(static_cast<elem*>(a.out) + rr.at * D + d, make_float4(v.x * f * g, v.y * f * g, v.z * f * g, v.w * f * g));
   if (a.lse && d == 0)
     a.lse[rr.at] = sum == 0.f ? -INFINITY : (M - kShift + log2f(sum)) * 0.69314718055994530942f;
 }

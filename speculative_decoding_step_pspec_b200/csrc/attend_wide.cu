@@ -273,9 +273,9 @@ __global__ void __launch_bounds__(kWideThreads, 2) attend_wide_kernel(const Atte
       }
       // 2^(14 - exponent of the row's largest element), kept within fp32's normal range
       const int ex = (int)(__float_as_uint(top) >> 23) - 127;
-      const int up = top == 0.f || ex == 128 ? 0 : min(100, 14 - ex);
+      const int up = top == 0.f || ex == 128 ? 0 : min(126, 14 - ex);
       const float f = __uint_as_float((unsigned)(127 + up) << 23);
-      mult = a.scale * kLog2e * (a.k_scale ? __ldg(a.k_scale + h) : 1.f) * __uint_as_float((unsigned)(127 - up) << 23);
+      mult = score_factor(a.scale, a.k_scale ? __ldg(a.k_scale + h) : 1.f, up);
 #pragma unroll 2
       for (int c = half * (D / 16); c < (half + 1) * (D / 16); ++c) {
         float x[8];

@@ -129,6 +129,35 @@ def test_attend_very_negative_scores_are_the_same_in_wide_tiles(D):
     assert torch.equal(narrow["out"][0], wide["out"][0]) and torch.isfinite(narrow["lse"]).all()
 
 
+@pytest.mark.parametrize("dtype,many", [(torch.bfloat16, False), (torch.bfloat16, True), (torch.float32, False)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_attend_at_the_ends_of_the_head_scales(D, dtype, many):
+    """A power of two moved between the queries and the keys' head scales changes nothing, one in the
+    values' only their power, as long as the outputs stay in fp32's normal range."""
+    rows = [40, 30] if many else [3, 1]
+    H = wide_heads(rows, 2, D) if many else 2
+    c = attend_case(D, rows, [300, 20000], 2 * H, H, D, 16, dtype, extra_rows=0)
+    cache, args = c["cache"], (i32(c["table"]), i32(c["qsl"]), i32(c["pos"]), i32(c["lens"]))
+    k, v = cache.k_scale.clone(), cache.v_scale.clone()
+    want = ps.attend(c["q"], cache, *args, want_lse=True)
+    for e in (-110, -60, 60, 100):
+        cache.k_scale = k * 2.0 ** e
+        got = ps.attend(c["q"] * 2.0 ** -e, cache, *args, want_lse=True)
+        assert torch.equal(got["out"], want["out"]) and torch.equal(got["lse"], want["lse"]), e
+    cache.k_scale = torch.full_like(k, 2.0 ** -20)
+    want = ps.attend(c["q"], cache, *args, want_lse=True)
+    cache.k_scale = torch.full_like(k, 2.0 ** -140)
+    got = ps.attend(c["q"] * 2.0 ** 120, cache, *args, want_lse=True)
+    assert torch.equal(got["out"], want["out"]) and torch.equal(got["lse"], want["lse"])
+    for e in (-100, 100):
+        cache.v_scale = v * 2.0 ** e
+        got = ps.attend(c["q"] * 2.0 ** 120, cache, *args, want_lse=True)
+        cache.v_scale = v
+        want = ps.attend(c["q"] * 2.0 ** 120, cache, *args, want_lse=True)
+        here = want["out"].double().abs() > 2.0 ** -25
+        assert torch.equal(got["out"].double()[here], (want["out"].double() * 2.0 ** e)[here])
+
+
 # --------------------------------------------------------------------------- append
 @pytest.mark.parametrize("rot", [0, 64])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
