@@ -40,7 +40,7 @@ constexpr int kGather = 4096;            // tokens that one CTA sorts
 constexpr int kPick = 1024;              // the largest rank looked for among the maxima
 constexpr int kChunk = 256;              // 32 lanes x 8 elements
 constexpr int kMaxCluster = 8;
-constexpr long long kFewRows = 32, kManyCtas = 1536;
+constexpr long long kFewRows = 32;
 constexpr int kBins = 4096;              // of a histogram
 constexpr int kListV = 65536;            // (1758 rows of 4928 logits, mixed filters: 214 us, 249 with lists)
 constexpr size_t kSliceBytes = 128 * 1024;   // a slice above this is read from global memory
@@ -1600,15 +1600,20 @@ cudaError_t launch_tag(FilterLaunch L, cudaStream_t stream) {
   const long long rows = (long long)L.a.B * L.a.K;
   const int chunks = (int)(((long long)L.a.V + Tag::kVec - 1 + kChunk - 1) / kChunk);   // at any alignment
   // Few rows: the most CTAs a row, its slices in shared memory (7 rows of 201088 bf16 logits: 21 us
-  // against 42 by one CTA a row).  Many: fewer CTAs a row, which meet less, and read it again
-  // from L2, where more loads are in flight than a slice in shared memory leaves room for (768
-  // such rows, mixed filters: 327 us by two CTAs, 390 by one, 490 by four; 988 by eight with slices,
-  // before the long rows started first).
+  // against 42 by one CTA a row; 64 rows of 5000, 69 us by two with slices, 79 without, so the border
+  // could lie higher).  Many: fewer CTAs a row, which meet less, and read it again from L2, where
+  // more loads are in flight than a slice in shared memory leaves room for.
   const bool few = rows <= kFewRows;
   int G = kMaxCluster;
-  // (a CTA's part of a row is not so short that meeting takes longer: 248 rows of 2371 tokens, top-p,
-  // 62 us by one CTA, 246 by four; 56 rows of 73585, 139 by four, 277 by eight)
-  while (G > 1 && (chunks < (few ? 16 : 64) * G || (!few && rows * G > kManyCtas))) G >>= 1;
+  // With many rows, G CTAs to one take G times the waves (of two CTAs an SM), each with its meetings,
+  // which are worth some 48 chunks of a CTA's part; the last rows end sooner by their longer parts.  Of
+  // 13 batches of 33 to 2000 rows x 8 vocabularies of 2300 to 201088 bf16 logits this takes 1.3 percent
+  // longer than the best G under mixed filters, 4 under any one (a fixed number of CTAs: 3 and 8).  E.g.
+  // mixed, us by one, two and four CTAs: 769 rows of 151936 427, 324, 497; 768 of 40000 157, 221, 368;
+  // 200 of 201088 353, 230, 204.
+  // (A CTA's part of a row is not so short that meeting takes longer: 248 rows of 2371 tokens, top-p,
+  // 62 us by one CTA, 246 by four.)
+  while (G > 1 && (chunks < (few ? 16 : 64) * G || (!few && rows * G * G * 48 > 2LL * kNumSMs * chunks))) G >>= 1;
   L.cluster = G;
   L.chunks_per_cta = (chunks + G - 1) / G;
   const size_t slice = (size_t)L.chunks_per_cta * kChunk * sizeof(typename Tag::elem);
