@@ -111,7 +111,6 @@ struct FilterSmem {
   double wide[kFW][kWays];
   int widei[kFW][kWays];
   unsigned long long cut;                 // CTA 0's answers to the cluster
-  double mass;
   float pick;
   int turn;                               // the exchange buffer of the next exchange
   int ok;
@@ -680,8 +679,8 @@ struct Filter {
     bool draw;               // draw the token (nothing is above the list)
     bool reach;              // the list must reach P, else it answers "not here"
   };
-  // With `reach` or without `draw`, whether the list held the cut, the cut and the list's mass go
-  // to every CTA's sm.ok, sm.cut and sm.mass, and the cluster barrier is arrived at.
+  // With `reach` or without `draw`, whether the list held the cut, the cut and the number of tokens up
+  // to it go to every CTA's sm.ok, sm.cut and sm.count, and the cluster barrier is arrived at.
   template <int kPer>
   __device__ void settle(int n, List q, double u) {
     FilterSmem& sm = *smem;
@@ -722,7 +721,6 @@ struct Filter {
         if (tid * kPer + r == m - 1)
           for (int g = 0; g < G; ++g) cluster_store(cluster_map(&sm.cut, g), key[r]);
       if (tid < G) {
-        cluster_store(cluster_map(&sm.mass, tid), (unsigned long long)__double_as_longlong(all));
         cluster_store32(cluster_map(&sm.ok, tid), ok);
         cluster_store32(cluster_map(&sm.count, tid), m);
       }
