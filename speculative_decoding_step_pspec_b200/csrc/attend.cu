@@ -452,8 +452,17 @@ attend_kernel(const AttendLaunch L) {
         for (int i = 0; i < 4; ++i)
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            mma16816(o[n][4 * k + i], fr[i], pb[n][0], pb[n][1]);
-            if constexpr (kF32) mma16816(o[n][4 * k + i], fr[i], pl[n][0], pl[n][1]);
+            if constexpr (kF32) {
+              // the step's sum by itself: the tensor cores cut a sum's last bits off, which along
+              // thousands of keys adds up (17792 keys: outputs off by 8e-6, added like this by 3e-6)
+              float x[4] = {};
+              mma16816(x, fr[i], pl[n][0], pl[n][1]);
+              mma16816(x, fr[i], pb[n][0], pb[n][1]);
+#pragma unroll
+              for (int c = 0; c < 4; ++c) o[n][4 * k + i][c] += x[c];
+            } else {
+              mma16816(o[n][4 * k + i], fr[i], pb[n][0], pb[n][1]);
+            }
           }
       }
       __syncwarp();                                         // the stage may be refilled

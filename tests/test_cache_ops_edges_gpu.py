@@ -158,6 +158,37 @@ def test_attend_at_the_ends_of_the_head_scales(D, dtype, many):
         assert torch.equal(got["out"].double()[here], (want["out"].double() * 2.0 ** e)[here])
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_attend_fp32_sums_along_many_keys(D):
+    """fp32 rows over thousands of keys in one go: off by what fp32 rounds, not by what the tensor cores
+    cut off.  Of outputs that are means of values of either sign, the relative error in the 2-norm is
+    about that of the weights (products and sums of scores of size 10, the exponential: 2^-20 of root
+    mean square) and that of some 300 additions in a row (2^-24 sqrt(300) = 2^-20)."""
+    B, H, n, bs = 64, 8, 20000, 16
+    g, pages = gen(D), n // bs
+    cache = random_cache(g, pages * 4, H, bs, D)                # (sequences share four sets of pages)
+    table = (torch.arange(B, device=DEV)[:, None] % 4 * pages + torch.arange(pages, device=DEV)).int()
+    q = torch.randn((B, H, D), generator=g, device=DEV) * 1.5
+    qsl, pos = torch.arange(B + 1, device=DEV).int(), torch.full((B,), n - 1, dtype=torch.int32, device=DEV)
+    o = ps.attend(q, cache, table, qsl, pos, pos + 1)
+    torch.cuda.synchronize()
+    levels = torch.tensor(R.LEVELS, device=DEV)
+    levels = torch.cat((levels, -levels))
+    err = ref = 0.0
+    for i in (0, 1, 63):
+        for h in (0, 7):
+            kv = []
+            for w in "kv":
+                b8 = getattr(cache, w)[table[i].long(), h].reshape(n, D // 2).int()
+                x = levels[torch.stack((b8 & 15, b8 >> 4), -1)].view(n, D // 16, 16)
+                x = x * getattr(cache, w + "_block_scales")[table[i].long(), h].double().view(n, D // 16, 1)
+                kv.append(x.view(n, D) * getattr(cache, w + "_scale")[h].double())
+            want = torch.softmax(kv[0] @ q[i, h].double() * D ** -0.5, 0) @ kv[1]
+            err += (o["out"][i, h].double() - want).square().sum().item()
+            ref += want.square().sum().item()
+    assert (err / ref) ** 0.5 <= 2.5e-6
+
+
 # --------------------------------------------------------------------------- append
 @pytest.mark.parametrize("rot", [0, 64])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
