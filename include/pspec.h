@@ -485,7 +485,8 @@ typedef enum { PSPEC_CACHE_ROWS = 0, PSPEC_CACHE_E2M1 = 1 } pspec_cache_kind;
  * rows of one call ends with bytes of either (the batch builder never does so); every other
  * slot of the cache keeps its content.
  * PSPEC_CACHE_ROWS stores the rows in their own dtype (pages [num_blocks, Hkv, block_size,
- * D], the scale arrays unused); PSPEC_CACHE_E2M1 stores the 4-bit form above.  k_out and
+ * D], the scale arrays unused), for a caller whose own attention reads them: pspec_attend reads
+ * the 4-bit form alone, which PSPEC_CACHE_E2M1 stores.  k_out and
  * v_out (optional, contiguous [T, Hkv, D], rows' dtype) receive the values the cache now
  * stands for, for callers that attend to the same chunk in 16 bits.
  * One launch.  Outputs must not overlap inputs (PSPEC_ERR_INVALID_ARG).  Limits: D a multiple
@@ -540,9 +541,12 @@ PSPEC_API pspec_status pspec_append_kv(const pspec_append_args *args, cudaStream
  * A row that sees no key gets zeros and lse = -inf.  Rows of kind PSPEC_ROW_REJ and
  * PSPEC_ROW_PAD (when row_kind is given), and rows of no sequence, are left as they were.
  * Statistics and sums are fp32; products of the cache's values (exact in fp16) with the
- * queries and the probabilities run on fp16 tensor cores with fp32 sums: bf16 queries are
- * exact there after a power-of-two scaling per row and probabilities are rounded to 11 bits;
- * fp32 queries and their probabilities are split into two fp16 terms.
+ * queries and the probabilities run on fp16 tensor cores with fp32 sums.  Rows are scaled by a
+ * power of two there, the largest element to between 2^14 and 2^15: a bf16 query's elements
+ * are exact down to 2^-31 of it, and off by at most 2^-39 of it below; probabilities are rounded
+ * to 11 bits (their sum is of unrounded ones).  fp32 queries and their probabilities are split
+ * into two such terms (22 bits), and their outputs summed outside the tensor cores, which cut
+ * a sum's last bits off.  A score beyond fp32's range is outside of what is computed.
  * D is 64 or 128 (PSPEC_ERR_UNSUPPORTED otherwise).  Invalid values on the device: a qsl that
  * is not an offset array into [0, T] skips the offending sequence (PSPEC_DEVERR_LAYOUT; a row
  * that two others then claim holds either's result); a
@@ -603,7 +607,8 @@ PSPEC_API pspec_status pspec_attend(const pspec_attend_args *args, void *workspa
  * exceeds uniforms[i][k] times the kept mass (if rounding leaves none, the last kept id with
  * mass), the convention of pspec_sample_drafts.  temperature 0 takes the argmax, lowest id on
  * ties.  Masses are fp64 sums of fp64 exponentials: a token is the exactly computed draw
- * unless its border is within about 1e-11 of the uniform.  NaN logits count as -inf; a row of
+ * unless its border is within about 1e-11 of the uniform, or a filter's limit within as much
+ * (relative) of a token's weight or of the mass before it.  NaN logits count as -inf; a row of
  * -inf alone gives token 0 with probability 0; if logits are +inf, those tokens share the
  * mass equally.  probs (optional) is the drawn token's share of the kept mass.  Any parameter
  * array may be NULL (temperature 1, filters off).  One launch, from a warp to a cluster of CTAs

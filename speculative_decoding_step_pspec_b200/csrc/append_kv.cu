@@ -15,9 +15,12 @@
 // significant bits) are exact, so that ties are seen as ties.
 //
 // Measured: 15360 rows (a quarter of them padding) of 64 query and 2 x 8 key and value heads of 64
-// bf16, to 4 bits with the stored values written out: 70 us, 3.5 TB/s or 53 percent of the measured
-// copy bandwidth.  Bound by instructions: 63 percent of the active issue slots, half of the integer
-// pipe.  A call for 15 rows takes 8 to 9 us, which is what a launch takes.
+// bf16, to 4 bits with the stored values written out: 68 us, 3.6 TB/s or 55 percent of the measured
+// copy bandwidth.  Neither bytes nor instructions fill it (64 percent of the active issue slots, half
+// of the integer pipe): 72 registers leave room for 31 percent of the warps, which wait for loads and
+// for one another's results.  A call for 15 rows takes 8 to 9 us from the host, which is its launch (a
+// call of padding rows alone takes as long); inside a graph 6.4 us, 1.1 with padding alone: one row's
+// chain of loads, angles and stores.  The 4-bit kernels spill up to 52 bytes, the fp64 step at most.
 #include <type_traits>
 
 #include "common.cuh"
@@ -92,8 +95,8 @@ __device__ __forceinline__ void values8(const uint4 (&raw)[Row<Tag>::kRaw], floa
   }
 }
 
-// Sine and cosine of the fp64 angle a, |a| < 2^31: reduced to |r| <= pi/4 by multiples of pi/2
-// (two terms of it), then the Taylor polynomials (remainders below 5e-17).
+// Sine and cosine of the fp64 angle a, |a| < 2^45: reduced to |r| <= pi/4 (and 2^-8) by multiples of
+// pi/2, whose two terms leave 2^44 * 1.5e-33 away, then the Taylor polynomials (remainders below 5e-17).
 __device__ __forceinline__ void turn_of(double a, double& sine, double& cosine) {
   const double n = rint(a * 0.63661977236758134308);
   double r = fma(-n, 1.57079632679489661923, a);
@@ -416,7 +419,7 @@ template <typename Tag>
 void launch_rows(const AppendLaunch& L, cudaStream_t stream) {
   const pspec_append_args& a = L.a;
   // A CTA to a row while there are few, else a warp: rows then wait for nothing but their own
-  // loads (15360 rows: 83 us, by CTAs of four rows 101).
+  // loads (15360 rows, both as first built: 83 us, by CTAs of four rows 101).
   const bool warps = a.T > 8 * kNumSMs && a.D <= 256;
   const int teams = warps ? block_of(32) / 32 : 1;
   const unsigned grid = (unsigned)(((long long)a.T + teams - 1) / teams);

@@ -19,11 +19,16 @@
 // interleaved are the pairs that the product with the values wants.  Dequantised values are
 // exact in fp16: 2 significant bits of the code times 4 of the scale, between 2^-10 and 2688.
 //
+// Probabilities go into the product as fp16: of 2^15 at most and 2^7 at a row's maximum, a bf16 row's
+// are rounded to 11 bits, an eighth of what its output is rounded by (they are summed as they are); an
+// fp32 row's, and its queries, are two such terms.  Its outputs are summed outside the products.
+//
 // Measured: one token of each of 64 sequences (540 thousand keys in all, 32 heads on 8, D = 128):
-// 179 us, 3.31 TB/s or half of the measured copy bandwidth; the conversions hold the integer pipe
-// at 56 percent and issue at 60, with three CTAs an SM (four: 188 us, five: 202, both for want of
-// registers).  One token over 100000 keys: 52 us, 33 of them at that rate, the
-// rest starting and joining the 55 parts of a tile.
+// 181 us, 3.27 TB/s or half of the measured copy bandwidth (fp32: 269 us); the conversions hold the
+// integer pipe at 55 percent and issue at 61, with three CTAs an SM (four: 188 us, five: 202, both for
+// want of registers), 18 percent of the warps.  One token over 100000 keys: 53 us, 33 of them at
+// that rate, the rest starting and joining the 55 parts of a tile.  Tiles of 8 rows spill nothing (fp32:
+// 8 bytes); bf16 tiles of 16 rows up to 208 bytes, of 32 rows up to 380.
 #include "attend_common.cuh"
 
 namespace pspec {
@@ -616,9 +621,9 @@ cudaError_t launch_nt(AttendLaunch L, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
-// The largest tiles that still give every CTA one: fewer leave each to many CTAs, whose results
-// take longer to join than a code takes to be converted again (8 rows of 64 heads over 4096 keys:
-// 23 us in tiles of 8 rows, 43 in tiles of 32).
+// The largest tiles of which there are three to an SM (about the CTAs that fit): fewer leave each to
+// many CTAs, whose results take longer to join than a code takes to be converted again (8 rows of 64
+// heads over 4096 keys: 23 us in tiles of 8 rows, 43 in tiles of 32).
 template <int D, typename Tag>
 cudaError_t launch_d(const AttendLaunch& L, cudaStream_t stream) {
   const long long rows = ((long long)L.a.T * (L.a.Hq / L.a.Hkv) + L.a.B - 1) / L.a.B;

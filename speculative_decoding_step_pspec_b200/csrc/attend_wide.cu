@@ -16,10 +16,15 @@
 // a unit took 2350 clocks of a CTA, the instructions of each one after another.  Warps without a
 // live row skip theirs.
 //
-// Measured: 64 draft batches (1 to 15 rows of 64 heads on 8 each, D = 64): 357 us, 166 TFLOP/s;
-// prompts of 200 to 700 rows (16 heads on 2, D = 128): 160 us, 220 TFLOP/s.  Instructions bound it:
-// a unit takes 2640 warp instructions before a second warp of softmax has live rows, most of them
-// in the conversions and around them; the tensor cores are busy for a fifth of the time.
+// Measured: 64 draft batches (1 to 15 rows of 64 heads on 8 each, D = 64): 361 us, 164 TFLOP/s;
+// prompts of 200 to 700 rows (16 heads on 2, D = 128): 161 us, 220 TFLOP/s.  Latency bounds it: a unit
+// takes 2640 warp instructions before a second warp of softmax has live rows, most of them in the
+// conversions and around them, which fill 61 (44) percent of the active issue slots with 48 percent of
+// the warps; the tensor cores are busy for 20 (14).  Among what is waited for are spilled registers:
+// 56 for every role, 348 bytes of spills for D = 64, 572 for D = 128.
+//
+// Probabilities are rounded to fp16 on their way into the product (11 bits, an eighth of the output's
+// rounding to bf16) and summed as they are.
 //
 // Every wait has a limit, after which the CTA goes on without waiting, sets PSPEC_DEVERR_WAIT and
 // ends as usual.

@@ -22,9 +22,11 @@
 // thousand.  Sums are joined in a fixed order, so results repeat.
 //
 // Measured: 448 rows of 151936 fp32 logits at their temperatures: 126 us, 2.2 TB/s or 33 percent of
-// the measured copy bandwidth; 33 instructions a logit, 8 of them fp64, fill 62 percent of the
-// active issue slots.  768 rows of 201088 bf16 logits, each request with its own filters: 327 us;
-// top-k alone 243, top-p alone 840 (its long nuclei 1100).  7 rows: 14 to 37 us.
+// the measured copy bandwidth; 35 instructions a logit, 8 of them fp64, in 60 percent of the active
+// issue slots with 42 percent of the warps: latency.  768 rows of 201088 bf16 logits, each request
+// with its own filters: 324 to 328 us; top-k alone 256, top-p alone 821.  7 rows: 14 to 57 us.
+// The streamed kernel holds 64 registers and spills 682 (fp32) or 786 bytes, its outlined steps up to
+// 1104.
 #include "filter_common.cuh"
 #include "kernels.h"
 #include "plan.h"
